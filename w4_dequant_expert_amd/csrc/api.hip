@@ -7,7 +7,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "route.h"
+#include "block.h"
 
 using namespace moe;
 
@@ -42,12 +42,6 @@ int check_device() {
   return st == 1 ? MOE_OK : MOE_EDEVICE;
 }
 
-}  // namespace moe
-
-namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int validate_dims(const moe_dims* d) {
   if (!d) return MOE_EINVAL;
   if (d->T < 0 || d->T > (1 << 20)) return MOE_EINVAL;
@@ -60,6 +54,34 @@ int validate_dims(const moe_dims* d) {
   if (d->tile_m_max < 16 || d->tile_m_max > 256 || d->tile_m_max % d->tile_gran) return MOE_EINVAL;
   return MOE_OK;
 }
+
+int validate_route_out(const moe_route_out* r, bool for_route) {
+  if (!r) return MOE_EINVAL;
+  if (!r->topk_idx || !r->topk_w || !r->counts || !r->offsets || !r->sorted_slot || !r->slot_pos ||
+      !r->blocks || !r->n_blocks || !r->status)
+    return MOE_EINVAL;
+  if (!aligned(r->topk_idx, 4) || !aligned(r->topk_w, 4) || !aligned(r->counts, 4) ||
+      !aligned(r->offsets, 4) || !aligned(r->sorted_slot, 4) || !aligned(r->slot_pos, 4) ||
+      !aligned(r->blocks, 16) || !aligned(r->n_blocks, 4) || !aligned(r->status, 4) ||
+      (r->logits && !aligned(r->logits, 4)))
+    return MOE_EALIGN;
+  if (for_route) {
+    if (!r->ws) return MOE_EINVAL;
+    if (!aligned(r->ws, 16)) return MOE_EALIGN;
+  }
+  return MOE_OK;
+}
+
+int32_t max_blocks_of(const moe_dims& d) {
+  const long long S = static_cast<long long>(d.T) * d.k;
+  long long nb = S / d.tile_m_max + (S < d.E ? S : d.E);
+  if (d.n_shared) nb += (d.T + d.tile_m_max - 1) / d.tile_m_max;
+  return static_cast<int32_t>(nb);
+}
+
+}  // namespace moe
+
+namespace {
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
@@ -88,23 +110,6 @@ WsLayout ws_layout(const moe_dims& d, bool need_logits) {
   return L;
 }
 
-int validate_route_out(const moe_route_out* r, bool for_route) {
-  if (!r) return MOE_EINVAL;
-  if (!r->topk_idx || !r->topk_w || !r->counts || !r->offsets || !r->sorted_slot || !r->slot_pos ||
-      !r->blocks || !r->n_blocks || !r->status)
-    return MOE_EINVAL;
-  if (!aligned(r->topk_idx, 4) || !aligned(r->topk_w, 4) || !aligned(r->counts, 4) ||
-      !aligned(r->offsets, 4) || !aligned(r->sorted_slot, 4) || !aligned(r->slot_pos, 4) ||
-      !aligned(r->blocks, 16) || !aligned(r->n_blocks, 4) || !aligned(r->status, 4) ||
-      (r->logits && !aligned(r->logits, 4)))
-    return MOE_EALIGN;
-  if (for_route) {
-    if (!r->ws) return MOE_EINVAL;
-    if (!aligned(r->ws, 16)) return MOE_EALIGN;
-  }
-  return MOE_OK;
-}
-
 int validate_bank(const moe_w4_bank* b) {
   if (!b || !b->gu || !b->dn) return MOE_EINVAL;
   if (!aligned(b->gu, 16) || !aligned(b->dn, 16)) return MOE_EALIGN;
@@ -119,13 +124,6 @@ BankView view(const moe_w4_bank* b) {
 
 bool pack_dims_ok(int32_t rows, int32_t K) {
   return rows > 0 && rows % 16 == 0 && rows <= (1 << 20) && K > 0 && K % 64 == 0 && K <= (1 << 16);
-}
-
-int32_t max_blocks_of(const moe_dims& d) {
-  const long long S = static_cast<long long>(d.T) * d.k;
-  long long nb = S / d.tile_m_max + (S < d.E ? S : d.E);
-  if (d.n_shared) nb += (d.T + d.tile_m_max - 1) / d.tile_m_max;
-  return static_cast<int32_t>(nb);
 }
 
 int validate_ffn_common(const moe_dims* d, const moe_route_out* r, const moe_w4_bank* routed,
@@ -158,8 +156,6 @@ GemmArgs gemm_args(const moe_dims& d, const moe_route_out* r, const moe_w4_bank*
   a.tile_gran = d.tile_gran;
   return a;
 }
-
-int launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ELAUNCH; }
 
 int validate_route_args(const moe_dims* d, const uint16_t* x, const float* w_router,
                         const float* logit_bias, const moe_route_out* out, bool need_ws) {

@@ -1,7 +1,8 @@
 """Python binding of libmoe_w4.so: argument marshalling only.
 
-Every call goes straight to the C ABI declared in include/moe_w4.h; all of the
-layer's arithmetic runs in the HIP kernels.  PyTorch is used only to allocate
+Every call goes straight to the C ABI declared in include/moe_w4.h,
+include/gdn_scan.h and include/moe_block.h; all of the layer's arithmetic runs
+in the HIP kernels.  PyTorch is used only to allocate
 device memory and to name the stream the kernels are enqueued on.  If the
 library is missing the import fails: there is no fallback path.
 """
@@ -26,7 +27,13 @@ EXPORTED = ("moe_abi_version", "moe_strerror", "moe_max_blocks", "moe_route_ws_b
             "moe_routed_w4_ffn", "moe_combine", "moe_w4_ffn_combine", "moe_w4_dequant",
             "moe_w4_dequant_packed", "moe_w4_packed_bytes",
             "moe_w4_pack", "moe_read_probe", "moe_mfma_probe", "gdn_scan",
-            "gdn_scan_chunked", "gdn_scan_chunked_ws_bytes")
+            "gdn_scan_chunked", "gdn_scan_chunked_ws_bytes", "moe_add_rmsnorm",
+            "moe_add_rmsnorm_backward", "moe_add_rmsnorm_backward_ws_bytes", "moe_q8_quantize",
+            "moe_q8_matmul", "moe_q8_gate_up", "moe_q8_down", "moe_dispatch_rows",
+            "moe_dispatch_rows_backward", "moe_combine_rows", "moe_combine_rows_backward")
+
+ELEM_F32, ELEM_BF16, ELEM_F16 = 0, 1, 2   # MOE_ELEM_*
+ELEM: dict = {}   # torch dtype -> MOE_ELEM_*, filled when the library is loaded
 
 
 class GdnDims(ctypes.Structure):
@@ -49,6 +56,22 @@ class RouteOut(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("topk_idx", "topk_w", "counts", "offsets",
                                                "sorted_slot", "slot_pos", "blocks", "n_blocks",
                                                "logits", "status", "ws")] + [("ws_bytes", ctypes.c_size_t)]
+
+
+class NormDims(ctypes.Structure):
+    """moe_norm_dims of include/moe_block.h; type is one of ELEM_*."""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class Q8Dims(ctypes.Structure):
+    """moe_q8_dims of include/moe_block.h; type is the output's."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "type")]
+
+
+class Q8Bank(ctypes.Structure):
+    """8-bit bank: gate/up and down matrices of n experts and their channel scales."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gu", "gu_s", "dn", "dn_s")]
 
 
 class MoeError(RuntimeError):
@@ -120,6 +143,27 @@ def lib():
         L.gdn_scan_chunked_ws_bytes.argtypes = [P(GdnDims)]
         L.gdn_scan.restype = ctypes.c_int
         L.gdn_scan.argtypes = [P(GdnDims), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        i32, size = ctypes.c_int32, ctypes.c_size_t
+        L.moe_add_rmsnorm.restype = ctypes.c_int
+        L.moe_add_rmsnorm.argtypes = [P(NormDims), vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_add_rmsnorm_backward_ws_bytes.restype = size
+        L.moe_add_rmsnorm_backward_ws_bytes.argtypes = [P(NormDims)]
+        L.moe_add_rmsnorm_backward.restype = ctypes.c_int
+        L.moe_add_rmsnorm_backward.argtypes = [P(NormDims), vp, vp, vp, vp, vp, vp, vp, size, vp]
+        L.moe_q8_quantize.restype = ctypes.c_int
+        L.moe_q8_quantize.argtypes = [P(NormDims), vp, vp, vp, vp]
+        L.moe_q8_matmul.restype = ctypes.c_int
+        L.moe_q8_matmul.argtypes = [P(Q8Dims), vp, vp, vp, vp, vp, vp]
+        L.moe_q8_gate_up.restype = ctypes.c_int
+        L.moe_q8_gate_up.argtypes = [P(Dims), vp, vp, P(RouteOut), P(Q8Bank), P(Q8Bank), vp, vp]
+        L.moe_q8_down.restype = ctypes.c_int
+        L.moe_q8_down.argtypes = [P(Dims), P(RouteOut), P(Q8Bank), P(Q8Bank), vp, vp, vp, vp]
+        for name in ("moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_rows"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [P(Dims), i32, vp, P(RouteOut), vp, vp]
+        L.moe_combine_rows_backward.restype = ctypes.c_int
+        L.moe_combine_rows_backward.argtypes = [P(Dims), i32, vp, vp, P(RouteOut), vp, vp, vp]
+        ELEM.update({torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.float16: ELEM_F16})
         _lib = L
     return _lib
 
@@ -262,6 +306,126 @@ def gdn_scan_chunked(d: GdnDims, q, k, v, g, beta, state_in, state_out, o, ws, w
                                   _stream(stream)), "gdn_scan_chunked")
 
 
+# ------------------------------------------- around the expert layer (include/moe_block.h)
+
+_ELEM_SIZE = (4, 2, 2)
+
+
+def _arg(t, nbytes: int, what: str):
+    """Address of a dense device array of at least nbytes (None -> NULL; raw addresses pass).
+
+    The C side cannot see sizes or strides, so tensors that are strided, too
+    small or off the current device are refused here."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: the tensor is on {t.device}, not on the current GPU")
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{what}: a contiguous tensor of at least {nbytes} bytes is needed, got "
+                         f"{tuple(t.shape)} {t.dtype} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _elem_bytes(elem: int) -> int:
+    return _ELEM_SIZE[elem] if 0 <= elem < 3 else 0   # an unknown type is refused by the C side
+
+
+def moe_add_rmsnorm(d: NormDims, x, res, weight, sum, y, yq=None, ys=None, stream=None):
+    """Residual addition and RMS norm (any of res, sum, y, yq with ys may be None)."""
+    n = d.T * d.H
+    row = n * _elem_bytes(d.type)
+    _check(lib().moe_add_rmsnorm(ctypes.byref(d), _arg(x, row, "x"), _arg(res, row, "res"),
+                                 _arg(weight, 4 * d.H, "weight"), _arg(sum, row, "sum"),
+                                 _arg(y, row, "y"), _arg(yq, n, "yq"), _arg(ys, 4 * d.T, "ys"),
+                                 _stream(stream)), "moe_add_rmsnorm")
+
+
+def moe_add_rmsnorm_backward_ws_bytes(d: NormDims) -> int:
+    return lib().moe_add_rmsnorm_backward_ws_bytes(ctypes.byref(d))
+
+
+def moe_add_rmsnorm_backward(d: NormDims, sum, weight, dy, dsum, dx, dweight, ws, ws_bytes: int,
+                             stream=None):
+    """Gradients of moe_add_rmsnorm (dsum and dweight may be None)."""
+    row = d.T * d.H * _elem_bytes(d.type)
+    _check(lib().moe_add_rmsnorm_backward(
+        ctypes.byref(d), _arg(sum, row, "sum"), _arg(weight, 4 * d.H, "weight"), _arg(dy, row, "dy"),
+        _arg(dsum, row, "dsum"), _arg(dx, row, "dx"), _arg(dweight, 4 * d.H, "dweight"),
+        _arg(ws, ws_bytes, "ws"), ws_bytes, _stream(stream)), "moe_add_rmsnorm_backward")
+
+
+def moe_q8_quantize(d: NormDims, x, xq, xs, stream=None):
+    """Rows to int8 with a scale per row."""
+    n = d.T * d.H
+    _check(lib().moe_q8_quantize(ctypes.byref(d), _arg(x, n * _elem_bytes(d.type), "x"),
+                                 _arg(xq, n, "xq"), _arg(xs, 4 * d.T, "xs"), _stream(stream)),
+           "moe_q8_quantize")
+
+
+def moe_q8_matmul(d: Q8Dims, xq, xs, wq, ws, out, stream=None):
+    """Dense product of 8-bit integers with token and channel scales."""
+    _check(lib().moe_q8_matmul(ctypes.byref(d), _arg(xq, d.M * d.K, "xq"), _arg(xs, 4 * d.M, "xs"),
+                               _arg(wq, d.N * d.K, "wq"), _arg(ws, 4 * d.N, "ws"),
+                               _arg(out, d.M * d.N * _elem_bytes(d.type), "out"), _stream(stream)),
+           "moe_q8_matmul")
+
+
+def _rows_of(d: Dims) -> int:
+    return d.T * (d.k + d.n_shared)
+
+
+def moe_q8_gate_up(d: Dims, xq, xs, out: RouteOut, routed: Q8Bank, shared, h, stream=None):
+    _check(lib().moe_q8_gate_up(ctypes.byref(d), _arg(xq, d.T * d.H, "xq"), _arg(xs, 4 * d.T, "xs"),
+                                ctypes.byref(out), ctypes.byref(routed),
+                                ctypes.byref(shared) if shared is not None else None,
+                                _arg(h, 2 * _rows_of(d) * d.I, "h"), _stream(stream)),
+           "moe_q8_gate_up")
+
+
+def moe_q8_down(d: Dims, out: RouteOut, routed: Q8Bank, shared, hq, hs, y_slots, stream=None):
+    rows = _rows_of(d)
+    _check(lib().moe_q8_down(ctypes.byref(d), ctypes.byref(out), ctypes.byref(routed),
+                             ctypes.byref(shared) if shared is not None else None,
+                             _arg(hq, rows * d.I, "hq"), _arg(hs, 4 * rows, "hs"),
+                             _arg(y_slots, 2 * rows * d.H, "y_slots"), _stream(stream)),
+           "moe_q8_down")
+
+
+def moe_dispatch_rows(d: Dims, elem: int, x, out: RouteOut, rows, stream=None):
+    """Token rows into moe_route's order (elem: one of ELEM_*)."""
+    e = _elem_bytes(elem) * d.H
+    _check(lib().moe_dispatch_rows(ctypes.byref(d), elem, _arg(x, d.T * e, "x"), ctypes.byref(out),
+                                   _arg(rows, _rows_of(d) * e, "rows"), _stream(stream)),
+           "moe_dispatch_rows")
+
+
+def moe_dispatch_rows_backward(d: Dims, elem: int, drows, out: RouteOut, dx, stream=None):
+    e = _elem_bytes(elem) * d.H
+    _check(lib().moe_dispatch_rows_backward(ctypes.byref(d), elem, _arg(drows, _rows_of(d) * e, "drows"),
+                                            ctypes.byref(out), _arg(dx, d.T * e, "dx"),
+                                            _stream(stream)), "moe_dispatch_rows_backward")
+
+
+def moe_combine_rows(d: Dims, elem: int, rows, out: RouteOut, y, stream=None):
+    """moe_combine for any row type."""
+    e = _elem_bytes(elem) * d.H
+    _check(lib().moe_combine_rows(ctypes.byref(d), elem, _arg(rows, _rows_of(d) * e, "rows"),
+                                  ctypes.byref(out), _arg(y, d.T * e, "y"), _stream(stream)),
+           "moe_combine_rows")
+
+
+def moe_combine_rows_backward(d: Dims, elem: int, dy, rows, out: RouteOut, drows, dtopk_w,
+                              stream=None):
+    """Gradients of the combine (dtopk_w None: rows is not read and may be None)."""
+    e = _elem_bytes(elem) * d.H
+    _check(lib().moe_combine_rows_backward(ctypes.byref(d), elem, _arg(dy, d.T * e, "dy"),
+                                           _arg(rows, _rows_of(d) * e, "rows"), ctypes.byref(out),
+                                           _arg(drows, _rows_of(d) * e, "drows"),
+                                           _arg(dtopk_w, 4 * d.T * d.k, "dtopk_w"),
+                                           _stream(stream)), "moe_combine_rows_backward")
+
+
 # --------------------------------------------------------------------- device buffers
 
 def make_dims(T, H, I, E, k, n_shared, tile_m_max=128, tile_gran=16) -> Dims:
@@ -312,6 +476,51 @@ class DeviceBank:
     def clone(self):
         return DeviceBank.from_tensors({k: v.clone() for k, v in self.t.items()}, self.n, self.H,
                                        self.I)
+
+    def nbytes(self) -> int:
+        return sum(v.numel() * v.element_size() for v in self.t.values())
+
+
+class DeviceBankQ8:
+    """An expert bank resident in device memory in 8 bits (moe_q8_bank).
+
+    gu [n][2I][H] (gate rows, then up rows) and dn [n][H][I] are float device
+    tensors; each output channel is quantised once by moe_q8_quantize.
+    """
+
+    def __init__(self, gu, dn):
+        n, two_i, H = gu.shape
+        self.n, self.H, self.I = n, H, two_i // 2
+        if dn.shape != (n, H, self.I):
+            raise ValueError(f"dn has shape {tuple(dn.shape)}, not {(n, H, self.I)}")
+        gq, gs = self._quantize(gu)
+        dq, ds = self._quantize(dn)
+        self.t = {"gu": gq, "gu_s": gs, "dn": dq, "dn_s": ds}
+        self.c = Q8Bank(*[self.t[k].data_ptr() for k in ("gu", "gu_s", "dn", "dn_s")])
+
+    @classmethod
+    def from_w4(cls, bank: dict, device="cuda"):
+        """From the canonical 4-bit arrays of a checkpoint (as DeviceBank takes them)."""
+        import torch
+        out = []
+        for half in ("gu", "dn"):
+            q, s, b = (_dev(bank[f"{half}_{p}"], device) for p in "qsb")
+            n, rows, half_k = q.shape
+            w = torch.empty((n, rows, 2 * half_k), dtype=torch.bfloat16, device=device)
+            moe_w4_dequant(n * rows, 2 * half_k, q, s, b, w)
+            torch.cuda.current_stream().synchronize()
+            out.append(w)
+        return cls(*out)
+
+    @staticmethod
+    def _quantize(w):
+        import torch
+        w = w.contiguous()
+        n, rows, K = w.shape
+        q = torch.empty((n, rows, K), dtype=torch.int8, device=w.device)
+        s = torch.empty((n, rows), dtype=torch.float32, device=w.device)
+        moe_q8_quantize(NormDims(n * rows, K, ELEM[w.dtype], 0.0), w, q, s)
+        return q, s
 
     def nbytes(self) -> int:
         return sum(v.numel() * v.element_size() for v in self.t.values())
@@ -435,4 +644,73 @@ class MoeLayer:
     def forward(self, x, y, routed=None, shared=None, stream=None):
         d = self.route(x, stream=stream)
         self.ffn_combine(d, x, y, routed, shared, stream)
+        return y
+
+    def _norm_buffers(self, device):
+        import torch
+        if getattr(self, "xn", None) is None:
+            self.xn = torch.empty((self.T_max, self.H), dtype=torch.int16, device=device)
+
+    def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
+        """The layer with what stands in front of it: res += x in place, then
+        the layer on the RMS norm of the sum (bfloat16 rows, one norm call)."""
+        d = self.dims(x.shape[0])
+        self._norm_buffers(x.device)
+        moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
+                        stream=stream)
+        return self.forward(self.xn[:d.T], y, stream=stream)
+
+
+class Q8MoeLayer(MoeLayer):
+    """The same layer with 8-bit banks (DeviceBankQ8): routing and combine as in
+    MoeLayer, the products in 8-bit integers.  forward(x, y) quantises the
+    tokens itself; forward_residual gets them from the norm."""
+
+    def __init__(self, *args, device="cuda", **kw):
+        import torch
+        super().__init__(*args, device=device, **kw)
+        rows = self.h.shape[0]
+        self.xq = torch.empty((self.T_max, self.H), dtype=torch.int8, device=device)
+        self.xs = torch.empty((self.T_max,), dtype=torch.float32, device=device)
+        self.hq = torch.empty((rows, self.I), dtype=torch.int8, device=device)
+        self.hs = torch.empty((rows,), dtype=torch.float32, device=device)
+
+    def gate_up(self, d, x, routed=None, shared=None, stream=None):
+        """h from the quantised tokens in xq and xs (x is not read)."""
+        r = routed or self.routed
+        s = shared or self.shared
+        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, r.c, s.c if s is not None else None, self.h,
+                       stream)
+
+    def down(self, d, routed=None, shared=None, stream=None):
+        r = routed or self.routed
+        s = shared or self.shared
+        moe_q8_quantize(NormDims(_rows_of(d), self.I, ELEM_BF16, 0.0), self.h, self.hq, self.hs, stream)
+        moe_q8_down(d, self.rt.c, r.c, s.c if s is not None else None, self.hq, self.hs, self.y_slots,
+                    stream)
+
+    def ffn(self, d, x, routed=None, shared=None, stream=None):
+        moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
+        self.gate_up(d, x, routed, shared, stream)
+        self.down(d, routed, shared, stream)
+
+    def shared_ffn(self, d, x, shared=None, stream=None):
+        raise NotImplementedError("the 8-bit layer has no split of the shared expert")
+
+    routed_ffn = shared_ffn
+
+    def ffn_combine(self, d, x, y, routed=None, shared=None, stream=None):
+        self.ffn(d, x, routed, shared, stream)
+        self.combine(d, y, stream)
+
+    def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
+        d = self.dims(x.shape[0])
+        self._norm_buffers(x.device)
+        moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
+                        self.xq, self.xs, stream)
+        xn = self.xn[:d.T]
+        self.route(xn, stream=stream)
+        self.gate_up(d, xn, stream=stream)
+        self.down(d, stream=stream)
+        self.combine(d, y, stream)
         return y
