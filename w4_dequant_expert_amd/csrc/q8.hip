@@ -6,19 +6,20 @@
 // the inputs in any order the two operands share, and every kernel here gives
 // the same bits.
 //
-// Two kernels, on v_mfma_i32_16x16x64_i8 (weights as the first operand, so a
-// lane ends with four neighbouring output channels of one row):
+// Two kernels, on the int8 matrix instructions (weights as the first operand,
+// so a lane ends with runs of four neighbouring output channels of one row):
 //   q8_stream_kernel: few rows.  Bound by reading the weights once; every wave
 //     streams its share of K straight from memory into the matrix operands,
 //     with no LDS and no barrier until the waves' sums are added.
 //   q8_tile_kernel: many rows.  Bound by the int8 matrix rate; tiles of both
-//     operands go through LDS in steps of 128 inputs.
+//     operands go through LDS in steps of 64 inputs.
 #include "block.h"
 
 namespace moe {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct Q8Args {
   const int8_t* x;
@@ -74,13 +75,14 @@ __device__ __forceinline__ int q8_source(const Q8Args& a, int row) {
   return (slot >= 0 && slot < S) ? slot / a.k : -1;
 }
 
-// The weight row of virtual column v.  SwiGLU pairs sixteen gate rows with
-// their sixteen up rows, so that one wave holds both in the same lanes.
-template <bool SWIGLU>
+// The weight row of virtual column v.  SwiGLU pairs W gate rows (the width of
+// a matrix tile) with their W up rows, so that one wave holds both in the same
+// lanes.
+template <bool SWIGLU, int W>
 __device__ __forceinline__ int q8_weight_row(int v, int N) {
   if (!SWIGLU) return min(v, N - 1);
-  const int half = N / 2, r = (v / 32) * 16 + (v & 15);
-  return (v & 16) ? min(half + r, N - 1) : min(r, half - 1);
+  const int half = N / 2, r = (v / (2 * W)) * W + v % W;
+  return (v & W) ? min(half + r, N - 1) : min(r, half - 1);
 }
 
 __device__ __forceinline__ void store4(void* out, size_t at, int type, const float (&v)[4]) {
@@ -93,32 +95,25 @@ __device__ __forceinline__ void store4(void* out, size_t at, int type, const flo
   }
 }
 
-// Four neighbouring outputs (columns v .. v+3) of one row from the integer sums.
-__device__ __forceinline__ void q8_store(const Q8Args& a, const float* __restrict__ ws, size_t row, int v,
-                                         float xs, i32x4 acc) {
-  if (v >= a.N) return;
-  const float4 s = *reinterpret_cast<const float4*>(ws + v);
-  const float o[4] = {static_cast<float>(acc[0]) * xs * s.x, static_cast<float>(acc[1]) * xs * s.y,
-                      static_cast<float>(acc[2]) * xs * s.z, static_cast<float>(acc[3]) * xs * s.w};
-  store4(a.out, row * a.N + v, a.type, o);
+// Four neighbouring outputs of one row from the integer sums; s their channels' scales.
+__device__ __forceinline__ void q8_scale(float xs, float4 s, i32x4 acc, float (&o)[4]) {
+  const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = static_cast<float>(acc[i]) * xs * f[i];
 }
 
-// silu(g) u for four neighbouring hidden columns c .. c+3 of one row.
-__device__ __forceinline__ void q8_store_swiglu(const Q8Args& a, const float* __restrict__ ws, size_t row,
-                                                int c, float xs, i32x4 g, i32x4 u) {
-  const int half = a.N / 2;
-  if (c >= half) return;
-  const float4 sg = *reinterpret_cast<const float4*>(ws + c);
-  const float4 su = *reinterpret_cast<const float4*>(ws + half + c);
-  const float fg[4] = {sg.x, sg.y, sg.z, sg.w}, fu[4] = {su.x, su.y, su.z, su.w};
-  float o[4];
+// silu(g) u of four neighbouring hidden columns.
+__device__ __forceinline__ void q8_swiglu(float xs, float4 sg, float4 su, i32x4 g, i32x4 u, float (&o)[4]) {
+  float gv[4], uv[4];
+  q8_scale(xs, sg, g, gv);
+  q8_scale(xs, su, u, uv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float gv = static_cast<float>(g[i]) * xs * fg[i];
-    const float uv = static_cast<float>(u[i]) * xs * fu[i];
-    o[i] = gv * __builtin_amdgcn_rcpf(1.0f + __expf(-gv)) * uv;
-  }
-  store4(a.out, row * half + c, MOE_ELEM_BF16, o);
+  for (int i = 0; i < 4; ++i) o[i] = gv[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-gv[i])) * uv[i];
+}
+
+// Scales of columns v .. v+3 (v a multiple of 4, N of 8); past N zeros.
+__device__ __forceinline__ float4 load_scales(const float* __restrict__ ws, int v, int N) {
+  return v < N ? *reinterpret_cast<const float4*>(ws + v) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 __device__ __forceinline__ i32x4 mfma(uint4 a, uint4 b, i32x4 c) {
@@ -126,13 +121,16 @@ __device__ __forceinline__ i32x4 mfma(uint4 a, uint4 b, i32x4 c) {
                                                0, 0, 0);
 }
 
+__device__ __forceinline__ i32x16 mfma32(uint4 a, uint4 b, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
+                                               0, 0, 0);
+}
+
 // ---------------------------------------------------------------------------
 // Few rows.  A workgroup of four waves owns CT*16 columns of a block and takes
 // its rows MT*16 at a time; wave w multiplies every fourth unit of 128 inputs.
-// Within a unit lane group q = lane/16 holds inputs 32q .. 32q+31 of its
-// weight row and of its token row (two 16-byte loads each, so a row's 128
-// bytes are read by neighbouring lanes at once); both operands agree on that
-// order, which is all the exact sum needs.  The four waves' sums meet in LDS.
+// A load covers 64 contiguous bytes of each of sixteen rows.  The four waves'
+// sums meet in LDS.
 // ---------------------------------------------------------------------------
 template <int CT, int MT, bool GROUPED, bool GATHER, bool SWIGLU>
 __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
@@ -155,7 +153,7 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
   const int8_t* wp[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c)
-    wp[c] = blk.w + static_cast<size_t>(q8_weight_row<SWIGLU>(v0 + c * 16 + r16, a.N)) * a.K;
+    wp[c] = blk.w + static_cast<size_t>(q8_weight_row<SWIGLU, 16>(v0 + c * 16 + r16, a.N)) * a.K;
   const int units = a.K / 128;  // whole units; K mod 128 = 64 leaves half of one
   for (int m0 = 0; m0 < blk.rows; m0 += MT * 16) {
     const int8_t* xp[MT];
@@ -170,17 +168,17 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[m][c] = i32x4{0, 0, 0, 0};
     for (int u = wave; u < units; u += 4) {
-      const int at = u * 128 + q * 32;
+      const int at = u * 128 + q * 16;
       uint4 wv[CT][2], xv[MT][2];
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
         wv[c][0] = *reinterpret_cast<const uint4*>(wp[c] + at);
-        wv[c][1] = *reinterpret_cast<const uint4*>(wp[c] + at + 16);
+        wv[c][1] = *reinterpret_cast<const uint4*>(wp[c] + at + 64);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         xv[m][0] = *reinterpret_cast<const uint4*>(xp[m] + at);
-        xv[m][1] = *reinterpret_cast<const uint4*>(xp[m] + at + 16);
+        xv[m][1] = *reinterpret_cast<const uint4*>(xp[m] + at + 64);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -220,37 +218,63 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
       }
       const float xs = a.xs[src];
       const int v = v0 + (i % CT) * 16;
-      if (SWIGLU)
-        q8_store_swiglu(a, blk.ws, row, v / 2 + 4 * q, xs, total(i), total(i + 1));
-      else
-        q8_store(a, blk.ws, row, v + 4 * q, xs, total(i));
+      float o[4];
+      if (SWIGLU) {
+        const int c = v / 2 + 4 * q, half = a.N / 2;
+        if (c >= half) continue;
+        q8_swiglu(xs, load_scales(blk.ws, c, half), load_scales(blk.ws + half, c, half), total(i), total(i + 1), o);
+        store4(a.out, static_cast<size_t>(row) * half + c, MOE_ELEM_BF16, o);
+      } else {
+        const int c = v + 4 * q;
+        if (c >= a.N) continue;
+        q8_scale(xs, load_scales(blk.ws, c, a.N), total(i), o);
+        store4(a.out, static_cast<size_t>(row) * a.N + c, a.type, o);
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  WM x WN waves own a tile of up to WM*MT*16 rows and WN*NT*16
-// columns; a wave multiplies mt (1..MT, from the block's rows) times NT tiles
-// of 16 x 16.  Both operands are copied straight from memory into LDS in steps
-// of 128 inputs, into two buffers in turn: the copies of step s+1 are in
-// flight while step s is multiplied.  A staged row is 128 bytes with its
-// 16-byte pieces XORed by the row (piece c of row r at c ^ (r mod 8)), so the
-// sixteen rows of an operand fragment spread over all banks; the copy puts
-// lane l's 16 bytes at byte 16 l, so the permutation is made by the address
-// each lane reads from.  Rows past the block repeat its last row and columns
-// past N the last column; they only reach outputs that are not stored.
+// Many rows.  WM x WN waves own a tile of up to WM*MT*32 rows and WN*NT*32
+// columns; a wave multiplies M (1..MT, from the block's rows) times NT tiles
+// of 32 x 32, by v_mfma_i32_32x32x32_i8: each operand register feeds twice the
+// products of the 16 x 16 form.
+//
+// K goes by in steps of 64 inputs through a ring of four LDS buffers.  Step s
+// begins with one barrier, after which the copies of step s+1 are in LDS and
+// nobody reads the buffer of step s-1 any more; the copies of step s+3 are
+// started into that one.  The operands of the first half of step s were read
+// from LDS during step s-1, so its products start at once, and the reads of
+// each half run under the products of the half before.
+//
+// A staged row is 64 bytes, its four 16-byte pieces permuted by the row (piece
+// c of row r at c ^ f(r), row_swizzle below) so that any eight or sixteen
+// neighbouring rows of a fragment cover different banks.  A copy moves sixteen
+// rows, lane l's 16 bytes landing at byte 16 l: the permutation is made by the
+// address each lane reads.  Rows past the block repeat its last row and
+// columns past N the last column; they only reach outputs that are not stored.
 //
 // Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8)
 // in contiguous runs, each run going through groups of four row blocks column
 // by column, so that the tiles an XCD works on together share rows and columns
 // in its own L2.
 // ---------------------------------------------------------------------------
-constexpr int kStep = 128;
+constexpr int kStep = 64;
 
-// This wave's copies have landed and every wave is here (one statement with a
-// memory clobber: no LDS access moves across it).
+__device__ __forceinline__ int row_swizzle(int r) {
+  return (((r >> 2) & 1) << 1) | (((r >> 1) ^ (r >> 3)) & 1);
+}
+
+// At most N of this wave's copies are still in flight, its LDS reads are done
+// and every wave is here.  The wait is the builtin, which the compiler's own
+// bookkeeping of waits takes into account; the empty statements keep LDS
+// accesses from moving across.
+template <int N>
 __device__ __forceinline__ void copies_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // What a wave of a tile keeps over the steps.
@@ -258,113 +282,202 @@ template <int WCOPY, int XCOPY>
 struct TileWave {
   const int8_t* wp[WCOPY];  // this lane's weight row in each of the wave's copies
   const int8_t* xp[XCOPY];  // and its token row
-  int xcopies;              // copies of token rows the workgroup makes
-  int piece;                // the bytes of a step this lane copies
   int wave, wm, wn, lane;
 };
 
+// 32 rows of a wave's outputs, from its sums to memory.  A lane holds, of each
+// tile of 32 columns, the columns 8g + 4hi .. +3 (g = 0..3) of row lane mod 32:
+// they go to LDS as rows, their 16-byte pieces XORed by the row against bank
+// conflicts, and come back as whole pieces in row order, so that a store
+// covers whole lines.  The wave uses LDS of its own, whose accesses stay in
+// order.  ok: this lane's row (lane mod 32) may be stored.
+template <int NT, bool SWIGLU, int TYPE>
+__device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk, const i32x16 (&acc)[NT], float xs,
+                                            uint8_t* out, int m1, int c0, int n_out, int lane, bool ok) {
+  constexpr int ELEM = TYPE == MOE_ELEM_F32 ? 4 : 2;
+  constexpr int COLS = (SWIGLU ? NT / 2 : NT) * 32, PIECES = COLS * ELEM / 16;
+  const int r32 = lane & 31, hi = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < NT; j += SWIGLU ? 2 : 1) {
+    const int cj = SWIGLU ? j / 2 * 32 : j * 32;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = cj + 8 * g + 4 * hi;
+      const i32x4 s0 = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+      float o[4];
+      if (SWIGLU) {
+        constexpr int P = SWIGLU ? 1 : 0;
+        const i32x4 s1 = {acc[j + P][4 * g], acc[j + P][4 * g + 1], acc[j + P][4 * g + 2], acc[j + P][4 * g + 3]};
+        q8_swiglu(xs, load_scales(blk.ws, c0 + c, n_out), load_scales(blk.ws + n_out, c0 + c, n_out), s0, s1, o);
+      } else {
+        q8_scale(xs, load_scales(blk.ws, c0 + c, n_out), s0, o);
+      }
+      const int byte = c * ELEM;
+      uint8_t* const to = out + r32 * PIECES * 16 + (((byte >> 4) ^ (r32 & (PIECES - 1))) << 4);
+      store4(to + (byte & 15), 0, TYPE, o);
+    }
+  }
+  asm volatile("" ::: "memory");
+  const uint64_t stored = __ballot(ok);
+#pragma unroll
+  for (int it = 0; it < 32 * PIECES / 64; ++it) {
+    const int r = (it * 64 + lane) / PIECES, piece = (it * 64 + lane) % PIECES;
+    const uint4 v = *reinterpret_cast<const uint4*>(out + r * PIECES * 16 + ((piece ^ (r & (PIECES - 1))) << 4));
+    const int c = c0 + piece * (16 / ELEM);
+    if (m1 + r < blk.rows && c < n_out && ((stored >> r) & 1))
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
+                                (static_cast<size_t>(blk.row0 + m1 + r) * n_out + c) * ELEM) = v;
+  }
+  asm volatile("" ::: "memory");
+}
+
 // One pass over K for M tiles of rows per wave, and their outputs.
-template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GATHER, bool SWIGLU>
+template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* buf0,
-                                             uint8_t* buf1) {
-  constexpr int WAVES = WM * WN, BN = WN * NT * 16;
-  const int nk = (a.K + kStep - 1) / kStep;
-  const int r16 = t.lane & 15, q = t.lane >> 4;
-  // byte of this lane's fragment piece within a 16-row tile: inputs 0..63 and 64..127 of a step
-  const int f0 = r16 * kStep + ((q ^ (r16 & 7)) << 4);
-  const int f1 = r16 * kStep + (((4 + q) ^ (r16 & 7)) << 4);
-  i32x4 acc[M][NT];
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
+                                             uint8_t* b2, uint8_t* b3) {
+  constexpr int WAVES = WM * WN, BN = WN * NT * 32, BM = XCOPY * 16 * WAVES;
+  // copies of token rows each wave makes, the same for all (so that the count
+  // of copies in flight is a constant): waves past the rows repeat the last row
+  constexpr int XC = (WM * M * 2 + WAVES - 1) / WAVES;
+  constexpr int COPIES = WCOPY + XC;
+  static_assert(XC <= XCOPY, "token copies");
+  const int nk = a.K / kStep;
+  const int r32 = t.lane & 31, hi = t.lane >> 5;
+  // byte of this lane's piece within a 32-row tile: inputs 0..31 and 32..63 of a step
+  const int f0 = r32 * kStep + ((hi ^ row_swizzle(r32)) << 4);
+  const int f1 = r32 * kStep + (((2 + hi) ^ row_swizzle(r32)) << 4);
+  i32x16 acc[M][NT];
 #pragma unroll
   for (int i = 0; i < M; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
   auto copy = [&](int s, uint8_t* buf) {
-    // the last step may hold 64 inputs: its second half repeats the first
-    // (read into LDS, never multiplied)
-    const int at = s * kStep + t.piece;
-    const int k0 = at < a.K ? at : at - 64;
 #pragma unroll
     for (int i = 0; i < WCOPY; ++i)
-      __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(t.wp[i] + s * kStep, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
 #pragma unroll
-    for (int i = 0; i < XCOPY; ++i)
-      if (i * WAVES + t.wave < t.xcopies)
-        __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0,
-                                         0);
+    for (int i = 0; i < XC; ++i)
+      __builtin_amdgcn_global_load_lds(t.xp[i] + s * kStep, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16,
+                                       0, 0);
   };
-  auto half = [&](const uint8_t* buf, int f) {
-    uint4 wf[NT], xf[M];
+  struct Frags {
+    uint4 w[NT], x[M];
+  };
+  auto read = [&](Frags& f, const uint8_t* buf, int at) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      wf[j] = *reinterpret_cast<const uint4*>(buf + (t.wn * NT + j) * 16 * kStep + f);
+      f.w[j] = *reinterpret_cast<const uint4*>(buf + (t.wn * NT + j) * 32 * kStep + at);
 #pragma unroll
     for (int i = 0; i < M; ++i)
-      xf[i] = *reinterpret_cast<const uint4*>(buf + (BN + (t.wm * M + i) * 16) * kStep + f);
+      f.x[i] = *reinterpret_cast<const uint4*>(buf + (BN + (t.wm * M + i) * 32) * kStep + at);
+  };
+  // products lo .. hi-1 of the wave's M * NT
+  auto multiply = [&](const Frags& f, int lo, int hi) {
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(wf[j], xf[i], acc[i][j]);
+      for (int j = 0; j < NT; ++j)
+        if (i * NT + j >= lo && i * NT + j < hi) acc[i][j] = mfma32(f.w[j], f.x[i], acc[i][j]);
   };
-  auto step = [&](int s, uint8_t* cur, uint8_t* next) {
-    copies_barrier();  // step s is in LDS; nobody reads `next` any more
+  Frags fa, fb;
+  // One step; full: the steps after next still have copies in flight and copies
+  // of their own to start.
+  auto step = [&](int s, bool full, uint8_t* cur, uint8_t* next, uint8_t* after) {
+    if (full || s + 2 < nk)
+      copies_barrier<COPIES>();
+    else
+      copies_barrier<0>();
     __builtin_amdgcn_sched_barrier(0);
-    if (s + 1 < nk) copy(s + 1, next);
+    if (full || s + 3 < nk) copy(s + 3, after);
+    read(fb, cur, f1);
     __builtin_amdgcn_sched_barrier(0);
-    half(cur, f0);
-    if (s * kStep + 64 < a.K) half(cur, f1);
+    multiply(fa, 0, M * NT);
+    // the wait for fb stands before its first product, ahead of the next reads
+    multiply(fb, 0, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (full || s + 1 < nk) read(fa, next, f0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(fb, 1, M * NT);
     __builtin_amdgcn_sched_barrier(0);
   };
-  copy(0, buf0);
-  for (int s = 0; s < nk; s += 2) {
-    step(s, buf0, buf1);
-    if (s + 1 < nk) step(s + 1, buf1, buf0);
+  copy(0, b0);
+  if (nk > 1) copy(1, b1);
+  if (nk > 2) copy(2, b2);
+  if (nk > 2)
+    copies_barrier<2 * COPIES>();
+  else
+    copies_barrier<0>();
+  read(fa, b0, f0);
+  int s = 0;
+  for (; s + 6 < nk; s += 4) {
+    step(s, true, b0, b1, b3);
+    step(s + 1, true, b1, b2, b0);
+    step(s + 2, true, b2, b3, b1);
+    step(s + 3, true, b3, b0, b2);
   }
+  for (; s < nk; s += 4) {
+    step(s, false, b0, b1, b3);
+    if (s + 1 < nk) step(s + 1, false, b1, b2, b0);
+    if (s + 2 < nk) step(s + 2, false, b2, b3, b1);
+    if (s + 3 < nk) step(s + 3, false, b3, b0, b2);
+  }
+  // Every wave has read its last operands: its share of the first two buffers
+  // holds its outputs, 32 rows at a time, on the way to whole-line stores.
+  copies_barrier<0>();
+  constexpr int kShare = (BN + BM) * kStep / (WAVES / 2);
+  uint8_t* const out = (t.wave < WAVES / 2 ? b0 : b1) + (t.wave % (WAVES / 2)) * kShare;
+  const int n_out = SWIGLU ? a.N / 2 : a.N;
+  const int c0 = (SWIGLU ? v0 / 2 : v0) + t.wn * (SWIGLU ? NT / 2 : NT) * 32;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
-    const int m = m0 + (t.wm * M + i) * 16 + r16;
-    if (m >= blk.rows) continue;
-    const int row = blk.row0 + m;
-    const int src = q8_source<GATHER>(a, row);
-    if (src < 0) {
-      status_set(a.status, MOE_STATUS_BAD_INDEX);
-      continue;
+    const int m1 = m0 + (t.wm * M + i) * 32;
+    if (m1 >= blk.rows) break;
+    const int src = q8_source<GATHER>(a, blk.row0 + min(m1 + r32, blk.rows - 1));
+    if (src < 0) status_set(a.status, MOE_STATUS_BAD_INDEX);
+    const float xs = a.xs[max(src, 0)];
+    if constexpr (!GROUPED) {
+      static_assert(32 * NT * 32 * 4 <= kShare, "a wave's outputs fit its share");
+      if (a.type == MOE_ELEM_F32) {
+        q8_tile_out<NT, SWIGLU, MOE_ELEM_F32>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, true);
+        continue;
+      } else if (a.type == MOE_ELEM_F16) {
+        q8_tile_out<NT, SWIGLU, MOE_ELEM_F16>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, true);
+        continue;
+      }
     }
-    const float xs = a.xs[src];
-#pragma unroll
-    for (int j = 0; j < NT; j += SWIGLU ? 2 : 1) {
-      const int v = v0 + (t.wn * NT + j) * 16;
-      if (SWIGLU)
-        q8_store_swiglu(a, blk.ws, row, v / 2 + 4 * q, xs, acc[i][j], acc[i][j + (SWIGLU ? 1 : 0)]);
-      else
-        q8_store(a, blk.ws, row, v + 4 * q, xs, acc[i][j]);
-    }
+    q8_tile_out<NT, SWIGLU, MOE_ELEM_BF16>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, !GATHER || src >= 0);
   }
 }
 
 // q8_tile_rows for mt (1..M) tiles of rows.
-template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GATHER, bool SWIGLU>
+template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_pick(int mt, const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* buf0,
-                                             uint8_t* buf1) {
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
+                                             uint8_t* b2, uint8_t* b3) {
   if constexpr (M > 1) {
     if (mt < M) {
-      q8_tile_pick<M - 1, WM, WN, NT, WCOPY, XCOPY, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, buf0, buf1);
+      q8_tile_pick<M - 1, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
       return;
     }
   }
-  q8_tile_rows<M, WM, WN, NT, WCOPY, XCOPY, GATHER, SWIGLU>(a, blk, m0, v0, t, buf0, buf1);
+  q8_tile_rows<M, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(a, blk, m0, v0, t, b0, b1, b2, b3);
 }
 
 template <int WM, int WN, int MT, int NT, bool GROUPED, bool GATHER, bool SWIGLU>
 __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
-  constexpr int WAVES = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
-  constexpr int WCOPY = BN / 8 / WAVES;  // copies of eight weight rows per wave and step
-  constexpr int XCOPY = BM / 8 / WAVES;  // of eight token rows, at most
-  static_assert(WCOPY * 8 * WAVES == BN && XCOPY * 8 * WAVES == BM, "whole copies");
-  // distinct arrays, so that reads of one do not wait for the copies into the other
-  __shared__ __attribute__((aligned(1024))) uint8_t buf0[(BN + BM) * kStep];
-  __shared__ __attribute__((aligned(1024))) uint8_t buf1[(BN + BM) * kStep];
+  constexpr int WAVES = WM * WN, BM = WM * MT * 32, BN = WN * NT * 32;
+  constexpr int WCOPY = BN / 16 / WAVES;  // copies of sixteen weight rows per wave and step
+  constexpr int XCOPY = BM / 16 / WAVES;  // of sixteen token rows, at most
+  static_assert(WCOPY * 16 * WAVES == BN && XCOPY * 16 * WAVES == BM, "whole copies");
+  static_assert(!SWIGLU || NT % 2 == 0, "gate and up columns come in pairs");
+  // distinct arrays, so that reads of one do not wait for the copies into another
+  __shared__ __attribute__((aligned(1024))) uint8_t b0[(BN + BM) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t b1[(BN + BM) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t b2[(BN + BM) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t b3[(BN + BM) * kStep];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = (a.N + BN - 1) / BN;
   const int nb = GROUPED ? min(*a.n_blocks, a.max_blocks) : (a.rows + BM - 1) / BM;
@@ -392,21 +505,23 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
   t.wave = wave;
   t.wm = wave / WN;
   t.wn = wave % WN;
-  t.piece = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int crow = lane >> 2, piece = ((lane & 3) ^ row_swizzle(crow)) * 16;
 #pragma unroll
   for (int i = 0; i < WCOPY; ++i)
     t.wp[i] = blk.w +
-              static_cast<size_t>(q8_weight_row<SWIGLU>(v0 + (i * WAVES + wave) * 8 + (lane >> 3), a.N)) * a.K;
+              static_cast<size_t>(q8_weight_row<SWIGLU, 32>(v0 + (i * WAVES + wave) * 16 + crow, a.N)) * a.K +
+              piece;
   for (int m0 = 0; m0 < blk.rows; m0 += BM) {
-    const int mt = (min(BM, blk.rows - m0) + WM * 16 - 1) / (WM * 16);
-    t.xcopies = 2 * WM * mt;
+    const int mt = (min(BM, blk.rows - m0) + WM * 32 - 1) / (WM * 32);
 #pragma unroll
     for (int i = 0; i < XCOPY; ++i) {
-      const int m = min(m0 + (i * WAVES + wave) * 8 + (lane >> 3), blk.rows - 1);
-      t.xp[i] = a.x + static_cast<size_t>(max(q8_source<GATHER>(a, blk.row0 + m), 0)) * a.K;
+      const int m = min(m0 + (i * WAVES + wave) * 16 + crow, blk.rows - 1);
+      t.xp[i] = a.x + static_cast<size_t>(max(q8_source<GATHER>(a, blk.row0 + m), 0)) * a.K + piece;
     }
-    q8_tile_pick<MT, WM, WN, NT, WCOPY, XCOPY, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, buf0, buf1);
-    __syncthreads();  // the buffers have been read before the next rows' copies
+    q8_tile_pick<MT, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
+    // before the next rows' copies the buffers have been read, and this wave's
+    // stores are out of the count that the copies are waited for by
+    copies_barrier<0>();
   }
 }
 
@@ -421,7 +536,7 @@ void launch_stream(const Q8Args& a, int blocks, hipStream_t s) {
 
 template <int WM, int WN, int MT, int NT, bool GROUPED, bool GATHER, bool SWIGLU>
 void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
-  const long long tiles = static_cast<long long>(blocks) * cdiv(a.N, WN * NT * 16);
+  const long long tiles = static_cast<long long>(blocks) * cdiv(a.N, WN * NT * 32);
   hipLaunchKernelGGL((q8_tile_kernel<WM, WN, MT, NT, GROUPED, GATHER, SWIGLU>),
                      dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
@@ -442,14 +557,14 @@ hipError_t launch_q8(const Q8Args& a, int rows_per_block, int blocks, int used, 
     }
   } else if (GROUPED) {
     if (rows_per_block <= 128)
-      launch_tile<2, 2, 4, 4, GROUPED, GATHER, SWIGLU>(a, blocks, s);
+      launch_tile<2, 2, 2, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s);
     else
-      launch_tile<2, 4, 8, 4, GROUPED, GATHER, SWIGLU>(a, blocks, s);
+      launch_tile<2, 4, 4, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s);
   } else {
     if (static_cast<long long>(cdiv(a.rows, 256)) * cdiv(a.N, 256) >= 256)
-      launch_tile<2, 4, 8, 4, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 256), s);
+      launch_tile<2, 4, 4, 2, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 256), s);
     else
-      launch_tile<2, 2, 4, 4, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 128), s);
+      launch_tile<2, 2, 2, 2, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 128), s);
   }
   return hipGetLastError();
 }
