@@ -12,7 +12,7 @@
 //     streams its share of K straight from memory into the matrix operands,
 //     with no LDS and no barrier until the waves' sums are added.
 //   q8_tile_kernel: many rows.  Bound by the int8 matrix rate; tiles of both
-//     operands go through LDS in steps of 64 inputs.
+//     operands go through LDS in steps of 128 inputs.
 #include "block.h"
 
 namespace moe {
@@ -240,39 +240,35 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
 // of 32 x 32, by v_mfma_i32_32x32x32_i8: each operand register feeds twice the
 // products of the 16 x 16 form.
 //
-// K goes by in steps of 64 inputs through a ring of four LDS buffers.  Step s
-// begins with one barrier, after which the copies of step s+1 are in LDS and
-// nobody reads the buffer of step s-1 any more; the copies of step s+3 are
-// started into that one.  The operands of the first half of step s were read
-// from LDS during step s-1, so its products start at once, and the reads of
-// each half run under the products of the half before.
+// K goes by in steps of 128 inputs (whole cache lines of both operands)
+// through two LDS buffers, each step in four quarters of 32 inputs.  The
+// operands of a quarter are read from LDS under the products of the quarter
+// before.  The one barrier of a step stands before the products of its last
+// quarter, whose operands are in registers by then: behind it the next step is
+// in LDS and nobody reads this step's buffer any more, so the copies of the
+// step after next start into it at once and have a whole step to land.
 //
-// A staged row is 64 bytes, its four 16-byte pieces permuted by the row (piece
-// c of row r at c ^ f(r), row_swizzle below) so that any eight or sixteen
-// neighbouring rows of a fragment cover different banks.  A copy moves sixteen
-// rows, lane l's 16 bytes landing at byte 16 l: the permutation is made by the
-// address each lane reads.  Rows past the block repeat its last row and
-// columns past N the last column; they only reach outputs that are not stored.
+// A staged row is 128 bytes, its 16-byte pieces XORed by the row (piece c of
+// row r at c ^ (r mod 8)), so that neighbouring rows of a fragment cover
+// different banks.  A copy moves eight rows, lane l's 16 bytes landing at byte
+// 16 l: the permutation is made by the address each lane reads.  Rows past the
+// block repeat its last row and columns past N the last column; they only
+// reach outputs that are not stored.
 //
 // Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8)
 // in contiguous runs, each run going through groups of four row blocks column
 // by column, so that the tiles an XCD works on together share rows and columns
 // in its own L2.
 // ---------------------------------------------------------------------------
-constexpr int kStep = 64;
+constexpr int kStep = 128;
 
-__device__ __forceinline__ int row_swizzle(int r) {
-  return (((r >> 2) & 1) << 1) | (((r >> 1) ^ (r >> 3)) & 1);
-}
-
-// At most N of this wave's copies are still in flight, its LDS reads are done
-// and every wave is here.  The wait is the builtin, which the compiler's own
-// bookkeeping of waits takes into account; the empty statements keep LDS
-// accesses from moving across.
-template <int N>
+// This wave's copies have landed, its LDS reads are done and every wave is
+// here.  The wait is the builtin, which the compiler's own bookkeeping of waits
+// takes into account; the empty statements keep LDS accesses from moving
+// across.
 __device__ __forceinline__ void copies_barrier() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -282,6 +278,7 @@ template <int WCOPY, int XCOPY>
 struct TileWave {
   const int8_t* wp[WCOPY];  // this lane's weight row in each of the wave's copies
   const int8_t* xp[XCOPY];  // and its token row
+  int piece;                // the bytes of a step this lane copies
   int wave, wm, wn, lane;
 };
 
@@ -292,8 +289,9 @@ struct TileWave {
 // covers whole lines.  The wave uses LDS of its own, whose accesses stay in
 // order.  ok: this lane's row (lane mod 32) may be stored.
 template <int NT, bool SWIGLU, int TYPE>
-__device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk, const i32x16 (&acc)[NT], float xs,
-                                            uint8_t* out, int m1, int c0, int n_out, int lane, bool ok) {
+__device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk, const i32x16 (&acc)[NT],
+                                            const float4 (&sc)[NT][4], float xs, uint8_t* out, int m1, int c0,
+                                            int n_out, int lane, bool ok) {
   constexpr int ELEM = TYPE == MOE_ELEM_F32 ? 4 : 2;
   constexpr int COLS = (SWIGLU ? NT / 2 : NT) * 32, PIECES = COLS * ELEM / 16;
   const int r32 = lane & 31, hi = lane >> 5;
@@ -308,9 +306,9 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
       if (SWIGLU) {
         constexpr int P = SWIGLU ? 1 : 0;
         const i32x4 s1 = {acc[j + P][4 * g], acc[j + P][4 * g + 1], acc[j + P][4 * g + 2], acc[j + P][4 * g + 3]};
-        q8_swiglu(xs, load_scales(blk.ws, c0 + c, n_out), load_scales(blk.ws + n_out, c0 + c, n_out), s0, s1, o);
+        q8_swiglu(xs, sc[j][g], sc[j + P][g], s0, s1, o);
       } else {
-        q8_scale(xs, load_scales(blk.ws, c0 + c, n_out), s0, o);
+        q8_scale(xs, sc[j][g], s0, o);
       }
       const int byte = c * ELEM;
       uint8_t* const to = out + r32 * PIECES * 16 + (((byte >> 4) ^ (r32 & (PIECES - 1))) << 4);
@@ -334,19 +332,11 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
 // One pass over K for M tiles of rows per wave, and their outputs.
 template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
-                                             uint8_t* b2, uint8_t* b3) {
-  constexpr int WAVES = WM * WN, BN = WN * NT * 32, BM = XCOPY * 16 * WAVES;
-  // copies of token rows each wave makes, the same for all (so that the count
-  // of copies in flight is a constant): waves past the rows repeat the last row
-  constexpr int XC = (WM * M * 2 + WAVES - 1) / WAVES;
-  constexpr int COPIES = WCOPY + XC;
-  static_assert(XC <= XCOPY, "token copies");
-  const int nk = a.K / kStep;
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1) {
+  constexpr int WAVES = WM * WN, BN = WN * NT * 32, BM = XCOPY * 8 * WAVES;
+  constexpr int XC = WM * M * 4;  // copies of token rows the workgroup makes
+  const int nk = (a.K + kStep - 1) / kStep;
   const int r32 = t.lane & 31, hi = t.lane >> 5;
-  // byte of this lane's piece within a 32-row tile: inputs 0..31 and 32..63 of a step
-  const int f0 = r32 * kStep + ((hi ^ row_swizzle(r32)) << 4);
-  const int f1 = r32 * kStep + (((2 + hi) ^ row_swizzle(r32)) << 4);
   i32x16 acc[M][NT];
 #pragma unroll
   for (int i = 0; i < M; ++i)
@@ -355,18 +345,24 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
   auto copy = [&](int s, uint8_t* buf) {
+    // the last step may hold 64 inputs: its second half repeats the first
+    // (read into LDS, never multiplied)
+    const int at = s * kStep + t.piece;
+    const int k0 = at < a.K ? at : at - 64;
 #pragma unroll
     for (int i = 0; i < WCOPY; ++i)
-      __builtin_amdgcn_global_load_lds(t.wp[i] + s * kStep, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
 #pragma unroll
-    for (int i = 0; i < XC; ++i)
-      __builtin_amdgcn_global_load_lds(t.xp[i] + s * kStep, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16,
-                                       0, 0);
+    for (int i = 0; i < XCOPY; ++i)
+      if ((i + 1) * WAVES <= XC || i * WAVES + t.wave < XC)
+        __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0, 0);
   };
   struct Frags {
     uint4 w[NT], x[M];
   };
-  auto read = [&](Frags& f, const uint8_t* buf, int at) {
+  // quarter q (inputs 32q .. 32q+31) of a step
+  auto read = [&](Frags& f, const uint8_t* buf, int q) {
+    const int at = r32 * kStep + (((2 * q + hi) ^ (r32 & 7)) << 4);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       f.w[j] = *reinterpret_cast<const uint4*>(buf + (t.wn * NT + j) * 32 * kStep + at);
@@ -383,101 +379,106 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
         if (i * NT + j >= lo && i * NT + j < hi) acc[i][j] = mfma32(f.w[j], f.x[i], acc[i][j]);
   };
   Frags fa, fb;
-  // One step; full: the steps after next still have copies in flight and copies
-  // of their own to start.
-  auto step = [&](int s, bool full, uint8_t* cur, uint8_t* next, uint8_t* after) {
-    if (full || s + 2 < nk)
-      copies_barrier<COPIES>();
-    else
-      copies_barrier<0>();
+  // One quarter: its products from f, quarter q of buf read into g behind the
+  // first of them (so that the wait for f stands ahead of the newer reads).
+  auto quarter = [&](const Frags& f, Frags& g, const uint8_t* buf, int q) {
+    multiply(f, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
-    if (full || s + 3 < nk) copy(s + 3, after);
-    read(fb, cur, f1);
+    read(g, buf, q);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(fa, 0, M * NT);
-    // the wait for fb stands before its first product, ahead of the next reads
-    multiply(fb, 0, 1);
+    multiply(f, 1, M * NT);
     __builtin_amdgcn_sched_barrier(0);
-    if (full || s + 1 < nk) read(fa, next, f0);
+  };
+  // Step s from its first quarter's operands in fa; leaves the next step's there.
+  auto step = [&](int s, uint8_t* cur, uint8_t* next) {
+    quarter(fa, fb, cur, 1);
+    if ((s + 1) * kStep <= a.K) {  // else 64 inputs: two quarters
+      quarter(fb, fa, cur, 2);
+      quarter(fa, fb, cur, 3);
+    }
+    copies_barrier();
+    if (s + 2 < nk) copy(s + 2, cur);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(fb, 1, M * NT);
+    if (s + 1 < nk) read(fa, next, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(fb, 0, M * NT);
     __builtin_amdgcn_sched_barrier(0);
   };
   copy(0, b0);
+  copies_barrier();
   if (nk > 1) copy(1, b1);
-  if (nk > 2) copy(2, b2);
-  if (nk > 2)
-    copies_barrier<2 * COPIES>();
-  else
-    copies_barrier<0>();
-  read(fa, b0, f0);
-  int s = 0;
-  for (; s + 6 < nk; s += 4) {
-    step(s, true, b0, b1, b3);
-    step(s + 1, true, b1, b2, b0);
-    step(s + 2, true, b2, b3, b1);
-    step(s + 3, true, b3, b0, b2);
+  read(fa, b0, 0);
+  for (int s = 0; s < nk; s += 2) {
+    step(s, b0, b1);
+    if (s + 1 < nk) step(s + 1, b1, b0);
   }
-  for (; s < nk; s += 4) {
-    step(s, false, b0, b1, b3);
-    if (s + 1 < nk) step(s + 1, false, b1, b2, b0);
-    if (s + 2 < nk) step(s + 2, false, b2, b3, b1);
-    if (s + 3 < nk) step(s + 3, false, b3, b0, b2);
-  }
-  // Every wave has read its last operands: its share of the first two buffers
-  // holds its outputs, 32 rows at a time, on the way to whole-line stores.
-  copies_barrier<0>();
+  // Every wave has read its last operands (the last step's barrier): its share
+  // of the buffers holds its outputs, 32 rows at a time, on the way to
+  // whole-line stores.
   constexpr int kShare = (BN + BM) * kStep / (WAVES / 2);
   uint8_t* const out = (t.wave < WAVES / 2 ? b0 : b1) + (t.wave % (WAVES / 2)) * kShare;
   const int n_out = SWIGLU ? a.N / 2 : a.N;
   const int c0 = (SWIGLU ? v0 / 2 : v0) + t.wn * (SWIGLU ? NT / 2 : NT) * 32;
+  // the scales of the wave's columns and rows, loaded together
+  float4 sc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = c0 + (SWIGLU ? j / 2 : j) * 32 + 8 * g + 4 * hi;
+      sc[j][g] = load_scales(blk.ws + (SWIGLU && j % 2 ? n_out : 0), c, n_out);
+    }
+  int srcs[M];
+  float xss[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    srcs[i] = q8_source<GATHER>(a, blk.row0 + min(m0 + (t.wm * M + i) * 32 + r32, blk.rows - 1));
+    xss[i] = a.xs[max(srcs[i], 0)];
+  }
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     const int m1 = m0 + (t.wm * M + i) * 32;
     if (m1 >= blk.rows) break;
-    const int src = q8_source<GATHER>(a, blk.row0 + min(m1 + r32, blk.rows - 1));
+    const int src = srcs[i];
     if (src < 0) status_set(a.status, MOE_STATUS_BAD_INDEX);
-    const float xs = a.xs[max(src, 0)];
+    const float xs = xss[i];
     if constexpr (!GROUPED) {
       static_assert(32 * NT * 32 * 4 <= kShare, "a wave's outputs fit its share");
       if (a.type == MOE_ELEM_F32) {
-        q8_tile_out<NT, SWIGLU, MOE_ELEM_F32>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, true);
+        q8_tile_out<NT, SWIGLU, MOE_ELEM_F32>(a, blk, acc[i], sc, xs, out, m1, c0, n_out, t.lane, true);
         continue;
       } else if (a.type == MOE_ELEM_F16) {
-        q8_tile_out<NT, SWIGLU, MOE_ELEM_F16>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, true);
+        q8_tile_out<NT, SWIGLU, MOE_ELEM_F16>(a, blk, acc[i], sc, xs, out, m1, c0, n_out, t.lane, true);
         continue;
       }
     }
-    q8_tile_out<NT, SWIGLU, MOE_ELEM_BF16>(a, blk, acc[i], xs, out, m1, c0, n_out, t.lane, !GATHER || src >= 0);
+    q8_tile_out<NT, SWIGLU, MOE_ELEM_BF16>(a, blk, acc[i], sc, xs, out, m1, c0, n_out, t.lane, !GATHER || src >= 0);
   }
 }
 
 // q8_tile_rows for mt (1..M) tiles of rows.
 template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_pick(int mt, const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
-                                             uint8_t* b2, uint8_t* b3) {
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1) {
   if constexpr (M > 1) {
     if (mt < M) {
-      q8_tile_pick<M - 1, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
+      q8_tile_pick<M - 1, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1);
       return;
     }
   }
-  q8_tile_rows<M, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(a, blk, m0, v0, t, b0, b1, b2, b3);
+  q8_tile_rows<M, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(a, blk, m0, v0, t, b0, b1);
 }
 
 template <int WM, int WN, int MT, int NT, bool GROUPED, bool GATHER, bool SWIGLU>
 __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
   constexpr int WAVES = WM * WN, BM = WM * MT * 32, BN = WN * NT * 32;
-  constexpr int WCOPY = BN / 16 / WAVES;  // copies of sixteen weight rows per wave and step
-  constexpr int XCOPY = BM / 16 / WAVES;  // of sixteen token rows, at most
-  static_assert(WCOPY * 16 * WAVES == BN && XCOPY * 16 * WAVES == BM, "whole copies");
+  constexpr int WCOPY = BN / 8 / WAVES;  // copies of eight weight rows per wave and step
+  constexpr int XCOPY = BM / 8 / WAVES;  // of eight token rows, at most
+  static_assert(WCOPY * 8 * WAVES == BN && XCOPY * 8 * WAVES == BM, "whole copies");
   static_assert(!SWIGLU || NT % 2 == 0, "gate and up columns come in pairs");
-  // distinct arrays, so that reads of one do not wait for the copies into another
+  // distinct arrays, so that reads of one do not wait for the copies into the other
   __shared__ __attribute__((aligned(1024))) uint8_t b0[(BN + BM) * kStep];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[(BN + BM) * kStep];
-  __shared__ __attribute__((aligned(1024))) uint8_t b2[(BN + BM) * kStep];
-  __shared__ __attribute__((aligned(1024))) uint8_t b3[(BN + BM) * kStep];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = (a.N + BN - 1) / BN;
   const int nb = GROUPED ? min(*a.n_blocks, a.max_blocks) : (a.rows + BM - 1) / BM;
@@ -505,23 +506,23 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
   t.wave = wave;
   t.wm = wave / WN;
   t.wn = wave % WN;
-  const int crow = lane >> 2, piece = ((lane & 3) ^ row_swizzle(crow)) * 16;
+  const int crow = lane >> 3;
+  t.piece = ((lane & 7) ^ crow) * 16;
 #pragma unroll
   for (int i = 0; i < WCOPY; ++i)
     t.wp[i] = blk.w +
-              static_cast<size_t>(q8_weight_row<SWIGLU, 32>(v0 + (i * WAVES + wave) * 16 + crow, a.N)) * a.K +
-              piece;
+              static_cast<size_t>(q8_weight_row<SWIGLU, 32>(v0 + (i * WAVES + wave) * 8 + crow, a.N)) * a.K;
   for (int m0 = 0; m0 < blk.rows; m0 += BM) {
     const int mt = (min(BM, blk.rows - m0) + WM * 32 - 1) / (WM * 32);
 #pragma unroll
     for (int i = 0; i < XCOPY; ++i) {
-      const int m = min(m0 + (i * WAVES + wave) * 16 + crow, blk.rows - 1);
-      t.xp[i] = a.x + static_cast<size_t>(max(q8_source<GATHER>(a, blk.row0 + m), 0)) * a.K + piece;
+      const int m = min(m0 + (i * WAVES + wave) * 8 + crow, blk.rows - 1);
+      t.xp[i] = a.x + static_cast<size_t>(max(q8_source<GATHER>(a, blk.row0 + m), 0)) * a.K;
     }
-    q8_tile_pick<MT, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
+    q8_tile_pick<MT, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1);
     // before the next rows' copies the buffers have been read, and this wave's
     // stores are out of the count that the copies are waited for by
-    copies_barrier<0>();
+    copies_barrier();
   }
 }
 
