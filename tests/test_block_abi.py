@@ -179,12 +179,16 @@ def test_row_refusals():
     assert g(b(d), 3, P[0], P[1], b(r), P[2], P[3], None) == -1
 
 
-def test_binding_refuses_host_tensors():
-    """A tensor that is not on the current GPU never reaches a kernel."""
-    if torch.cuda.is_available():
-        pytest.skip("checked without a GPU")
+def test_binding_refuses_host_strided_and_short_tensors():
+    """What the C side could not see never reaches a kernel."""
     _arg = moe.moe._arg
-    assert _arg(None, 16, "x") is None and _arg(4096, 16, "x") == 4096
+    assert _arg(None, 16, "x", 0) is None and _arg(4096, 16, "x", 0) == 4096
+    x = torch.zeros((4, 4))
+    host = x.get_device()   # -1
+    assert _arg(x, 64, "x", host) == x.data_ptr()
+    for t, n, dev in ((x, 64, 0), (x, 65, host), (x.t(), 64, host), (x[:, :2], 32, host)):
+        with pytest.raises(ValueError):
+            _arg(t, n, "x", dev)
 
 
 # ------------------------------------------------------------------ the references themselves

@@ -47,9 +47,12 @@ struct Q8Block {
   int row0, rows;
 };
 
-// Block b of the map; false (with the status bit) for an entry out of range.
+// Block b < max_blocks of the map; false past its end, and (with the status
+// bit) for an entry out of range.  The entry and the map's length are loaded
+// together.
 __device__ __forceinline__ bool q8_block(const Q8Args& a, int b, Q8Block& o) {
   const int4 e = reinterpret_cast<const int4*>(a.blocks)[b];
+  if (b >= *a.n_blocks) return false;
   const int g = uniform(e.x);
   o.row0 = uniform(e.y);
   o.rows = uniform(e.z);
@@ -127,15 +130,15 @@ __device__ __forceinline__ i32x16 mfma32(uint4 a, uint4 b, i32x16 c) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows.  A workgroup of four waves owns CT*16 columns of a block and takes
-// its rows MT*16 at a time; wave w multiplies every fourth unit of 128 inputs.
-// A load covers 64 contiguous bytes of each of sixteen rows.  The four waves'
-// sums meet in LDS.
+// Few rows.  A workgroup of W waves owns CT*16 columns of a block and takes its
+// rows MT*16 at a time; wave w multiplies every W-th unit of 128 inputs.  A load
+// covers 64 contiguous bytes of each of sixteen rows.  The waves' sums meet in
+// LDS.
 // ---------------------------------------------------------------------------
-template <int CT, int MT, bool GROUPED, bool GATHER, bool SWIGLU>
-__global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
+template <int W, int CT, int MT, bool GROUPED, bool GATHER, bool SWIGLU>
+__global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
   static_assert(!SWIGLU || CT % 2 == 0, "gate and up columns come in pairs");
-  __shared__ i32x4 part[4][MT * CT][64];
+  __shared__ i32x4 part[W][MT * CT][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
   const int nt = (a.N + CT * 16 - 1) / (CT * 16);
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
   const int v0 = (blockIdx.x % nt) * CT * 16;
   Q8Block blk;
   if (GROUPED) {
-    if (b >= min(*a.n_blocks, a.max_blocks) || !q8_block(a, b, blk)) return;
+    if (!q8_block(a, b, blk)) return;
   } else {
     blk.w = a.w;
     blk.ws = a.ws;
@@ -153,48 +156,48 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
   const int8_t* wp[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c)
-    wp[c] = blk.w + static_cast<size_t>(q8_weight_row<SWIGLU, 16>(v0 + c * 16 + r16, a.N)) * a.K;
-  const int units = a.K / 128;  // whole units; K mod 128 = 64 leaves half of one
+    wp[c] = blk.w + static_cast<size_t>(q8_weight_row<SWIGLU, 16>(v0 + c * 16 + r16, a.N)) * a.K + q * 16;
+  const int units = (a.K + 127) / 128;
   for (int m0 = 0; m0 < blk.rows; m0 += MT * 16) {
     const int8_t* xp[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int src = q8_source<GATHER>(a, blk.row0 + min(m0 + m * 16 + r16, blk.rows - 1));
-      xp[m] = a.x + static_cast<size_t>(max(src, 0)) * a.K;
-    }
     i32x4 acc[MT][CT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[m][c] = i32x4{0, 0, 0, 0};
-    for (int u = wave; u < units; u += 4) {
-      const int at = u * 128 + q * 16;
+    for (int u = wave; u < units; u += W) {
       uint4 wv[CT][2], xv[MT][2];
+      const int at = u * 128;
+      const bool whole = at + 64 < a.K;         // the last unit may hold 64 inputs,
+      const int second = whole ? at + 64 : at;  // which are then not multiplied twice
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
         wv[c][0] = *reinterpret_cast<const uint4*>(wp[c] + at);
-        wv[c][1] = *reinterpret_cast<const uint4*>(wp[c] + at + 64);
+        wv[c][1] = *reinterpret_cast<const uint4*>(wp[c] + second);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (u == wave) {
+        // the tokens' addresses wait for the routing tables: behind the first
+        // weight loads, which do not
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int src = q8_source<GATHER>(a, blk.row0 + min(m0 + m * 16 + r16, blk.rows - 1));
+          xp[m] = a.x + static_cast<size_t>(max(src, 0)) * a.K + q * 16;
+        }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         xv[m][0] = *reinterpret_cast<const uint4*>(xp[m] + at);
-        xv[m][1] = *reinterpret_cast<const uint4*>(xp[m] + at + 64);
+        xv[m][1] = *reinterpret_cast<const uint4*>(xp[m] + second);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !whole) break;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int c = 0; c < CT; ++c) acc[m][c] = mfma(wv[c][h], xv[m][h], acc[m][c]);
-    }
-    if ((a.K & 64) && wave == (units & 3)) {
-      const int at = units * 128 + q * 16;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(xp[m] + at);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          acc[m][c] = mfma(*reinterpret_cast<const uint4*>(wp[c] + at), xv, acc[m][c]);
       }
     }
     if (m0) __syncthreads();  // the sums of the rows before have been read
@@ -204,10 +207,13 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
       for (int c = 0; c < CT; ++c) part[wave][m * CT + c][lane] = acc[m][c];
     __syncthreads();
     auto total = [&](int i) {
-      return part[0][i][lane] + part[1][i][lane] + part[2][i][lane] + part[3][i][lane];
+      i32x4 s = part[0][i][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) s += part[w][i][lane];
+      return s;
     };
     constexpr int STEP = SWIGLU ? 2 : 1;
-    for (int i = wave * STEP; i < MT * CT; i += 4 * STEP) {
+    for (int i = wave * STEP; i < MT * CT; i += W * STEP) {
       const int m = m0 + (i / CT) * 16 + r16;
       if (m >= blk.rows) continue;
       const int row = blk.row0 + m;
@@ -241,12 +247,12 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
 // products of the 16 x 16 form.
 //
 // K goes by in steps of 128 inputs (whole cache lines of both operands)
-// through two LDS buffers, each step in four quarters of 32 inputs.  The
-// operands of a quarter are read from LDS under the products of the quarter
+// through a ring of R LDS buffers, each step in four quarters of 32 inputs.
+// The operands of a quarter are read from LDS under the products of the quarter
 // before.  The one barrier of a step stands before the products of its last
 // quarter, whose operands are in registers by then: behind it the next step is
-// in LDS and nobody reads this step's buffer any more, so the copies of the
-// step after next start into it at once and have a whole step to land.
+// in LDS and nobody reads this step's buffer any more, so the copies of step
+// s + R start into it at once and have R - 1 steps to land.
 //
 // A staged row is 128 bytes, its 16-byte pieces XORed by the row (piece c of
 // row r at c ^ (r mod 8)), so that neighbouring rows of a fragment cover
@@ -262,13 +268,14 @@ __global__ __launch_bounds__(256) void q8_stream_kernel(Q8Args a) {
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 
-// This wave's copies have landed, its LDS reads are done and every wave is
-// here.  The wait is the builtin, which the compiler's own bookkeeping of waits
+// At most N of this wave's copies are still in flight, its LDS reads are done
+// and every wave is here.  The wait is the builtin, which the compiler's own bookkeeping of waits
 // takes into account; the empty statements keep LDS accesses from moving
 // across.
+template <int N>
 __device__ __forceinline__ void copies_barrier() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -330,11 +337,16 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
 }
 
 // One pass over K for M tiles of rows per wave, and their outputs.
-template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
+template <int M, int WM, int WN, int NT, int R, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1) {
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
+                                             uint8_t* b2, uint8_t* b3) {
   constexpr int WAVES = WM * WN, BN = WN * NT * 32, BM = XCOPY * 8 * WAVES;
-  constexpr int XC = WM * M * 4;  // copies of token rows the workgroup makes
+  // copies of token rows each wave makes, the same for all (so that the copies
+  // in flight are a known number): past the rows they repeat the last row
+  constexpr int XC = (WM * M * 4 + WAVES - 1) / WAVES;
+  constexpr int COPIES = WCOPY + XC;
+  static_assert(XC <= XCOPY && (R - 2) * COPIES < 64, "copies in flight fit the wait's field");
   const int nk = (a.K + kStep - 1) / kStep;
   const int r32 = t.lane & 31, hi = t.lane >> 5;
   i32x16 acc[M][NT];
@@ -353,9 +365,8 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
     for (int i = 0; i < WCOPY; ++i)
       __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
 #pragma unroll
-    for (int i = 0; i < XCOPY; ++i)
-      if ((i + 1) * WAVES <= XC || i * WAVES + t.wave < XC)
-        __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+    for (int i = 0; i < XC; ++i)
+      __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0, 0);
   };
   struct Frags {
     uint4 w[NT], x[M];
@@ -389,29 +400,42 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
     multiply(f, 1, M * NT);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Step s from its first quarter's operands in fa; leaves the next step's there.
-  auto step = [&](int s, uint8_t* cur, uint8_t* next) {
+  // Step s from its first quarter's operands in fa; leaves the next step's
+  // there.  full: the R - 1 steps after it are there.
+  auto step = [&](int s, bool full, uint8_t* cur, uint8_t* next) {
     quarter(fa, fb, cur, 1);
     if ((s + 1) * kStep <= a.K) {  // else 64 inputs: two quarters
       quarter(fb, fa, cur, 2);
       quarter(fa, fb, cur, 3);
     }
-    copies_barrier();
-    if (s + 2 < nk) copy(s + 2, cur);
+    if (full || s + R - 1 < nk)
+      copies_barrier<(R - 2) * COPIES>();
+    else
+      copies_barrier<0>();
+    if (s + R < nk) copy(s + R, cur);
     __builtin_amdgcn_sched_barrier(0);
-    if (s + 1 < nk) read(fa, next, 0);
+    if (full || s + 1 < nk) read(fa, next, 0);
     __builtin_amdgcn_sched_barrier(0);
     multiply(fb, 0, M * NT);
     __builtin_amdgcn_sched_barrier(0);
   };
-  copy(0, b0);
-  copies_barrier();
-  if (nk > 1) copy(1, b1);
+  uint8_t* const ring[4] = {b0, b1, b2, b3};
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (i < nk) copy(i, ring[i]);
+  if (nk >= R)
+    copies_barrier<(R - 1) * COPIES>();
+  else
+    copies_barrier<0>();
   read(fa, b0, 0);
-  for (int s = 0; s < nk; s += 2) {
-    step(s, b0, b1);
-    if (s + 1 < nk) step(s + 1, b1, b0);
-  }
+  int s = 0;
+  for (; s + 2 * R - 2 < nk; s += R)
+#pragma unroll
+    for (int i = 0; i < R; ++i) step(s + i, true, ring[i], ring[(i + 1) % R]);
+  for (; s < nk; s += R)
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (s + i < nk) step(s + i, false, ring[i], ring[(i + 1) % R]);
   // Every wave has read its last operands (the last step's barrier): its share
   // of the buffers holds its outputs, 32 rows at a time, on the way to
   // whole-line stores.
@@ -457,20 +481,21 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
 }
 
 // q8_tile_rows for mt (1..M) tiles of rows.
-template <int M, int WM, int WN, int NT, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
+template <int M, int WM, int WN, int NT, int R, int WCOPY, int XCOPY, bool GROUPED, bool GATHER, bool SWIGLU>
 __device__ __forceinline__ void q8_tile_pick(int mt, const Q8Args& a, const Q8Block& blk, int m0, int v0,
-                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1) {
+                                             const TileWave<WCOPY, XCOPY>& t, uint8_t* b0, uint8_t* b1,
+                                             uint8_t* b2, uint8_t* b3) {
   if constexpr (M > 1) {
     if (mt < M) {
-      q8_tile_pick<M - 1, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1);
+      q8_tile_pick<M - 1, WM, WN, NT, R, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
       return;
     }
   }
-  q8_tile_rows<M, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(a, blk, m0, v0, t, b0, b1);
+  q8_tile_rows<M, WM, WN, NT, R, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(a, blk, m0, v0, t, b0, b1, b2, b3);
 }
 
-template <int WM, int WN, int MT, int NT, bool GROUPED, bool GATHER, bool SWIGLU>
-__global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
+template <int WM, int WN, int MT, int NT, int R, bool GROUPED, bool GATHER, bool SWIGLU>
+__global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
   constexpr int WAVES = WM * WN, BM = WM * MT * 32, BN = WN * NT * 32;
   constexpr int WCOPY = BN / 8 / WAVES;  // copies of eight weight rows per wave and step
   constexpr int XCOPY = BM / 8 / WAVES;  // of eight token rows, at most
@@ -479,8 +504,11 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
   // distinct arrays, so that reads of one do not wait for the copies into the other
   __shared__ __attribute__((aligned(1024))) uint8_t b0[(BN + BM) * kStep];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[(BN + BM) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t b2[R > 2 ? (BN + BM) * kStep : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t b3[R > 3 ? (BN + BM) * kStep : 16];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = (a.N + BN - 1) / BN;
+  static_assert(R >= 2 && R <= 4, "buffers");
   const int nb = GROUPED ? min(*a.n_blocks, a.max_blocks) : (a.rows + BM - 1) / BM;
   int b, ni;
   {
@@ -519,66 +547,91 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(Q8Args a) {
       const int m = min(m0 + (i * WAVES + wave) * 8 + crow, blk.rows - 1);
       t.xp[i] = a.x + static_cast<size_t>(max(q8_source<GATHER>(a, blk.row0 + m), 0)) * a.K;
     }
-    q8_tile_pick<MT, WM, WN, NT, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1);
+    q8_tile_pick<MT, WM, WN, NT, R, WCOPY, XCOPY, GROUPED, GATHER, SWIGLU>(mt, a, blk, m0, v0, t, b0, b1, b2, b3);
     // before the next rows' copies the buffers have been read, and this wave's
     // stores are out of the count that the copies are waited for by
-    copies_barrier();
+    copies_barrier<0>();
   }
 }
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <int CT, int MT, bool GROUPED, bool GATHER, bool SWIGLU>
+template <int W, int CT, int MT, bool GROUPED, bool GATHER, bool SWIGLU>
 void launch_stream(const Q8Args& a, int blocks, hipStream_t s) {
   const long long n = static_cast<long long>(blocks) * cdiv(a.N, CT * 16);
-  hipLaunchKernelGGL((q8_stream_kernel<CT, MT, GROUPED, GATHER, SWIGLU>), dim3(static_cast<unsigned>(n)),
-                     dim3(256), 0, s, a);
+  hipLaunchKernelGGL((q8_stream_kernel<W, CT, MT, GROUPED, GATHER, SWIGLU>), dim3(static_cast<unsigned>(n)),
+                     dim3(64 * W), 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT, bool GROUPED, bool GATHER, bool SWIGLU>
+template <int WM, int WN, int MT, int NT, int R, bool GROUPED, bool GATHER, bool SWIGLU>
 void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
   const long long tiles = static_cast<long long>(blocks) * cdiv(a.N, WN * NT * 32);
-  hipLaunchKernelGGL((q8_tile_kernel<WM, WN, MT, NT, GROUPED, GATHER, SWIGLU>),
+  hipLaunchKernelGGL((q8_tile_kernel<WM, WN, MT, NT, R, GROUPED, GATHER, SWIGLU>),
                      dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
 
-// rows_per_block: rows a block is expected to hold; blocks: the most there can
-// be; used: blocks expected to be there.
-template <bool GROUPED, bool GATHER, bool SWIGLU>
-hipError_t launch_q8(const Q8Args& a, int rows_per_block, int blocks, int used, hipStream_t s) {
-  if (rows_per_block <= 32) {
-    const bool two = rows_per_block > 16;
-    const long long columns = static_cast<long long>(used) * (a.N / 16);
-    if (columns >= 4 * 512) {
-      two ? launch_stream<4, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s)
-          : launch_stream<4, 1, GROUPED, GATHER, SWIGLU>(a, blocks, s);
-    } else {
-      two ? launch_stream<2, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s)
-          : launch_stream<2, 1, GROUPED, GATHER, SWIGLU>(a, blocks, s);
-    }
-  } else if (GROUPED) {
-    if (rows_per_block <= 128)
-      launch_tile<2, 2, 2, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s);
+// Which kernel.  Every one of them takes any block (rows past its tile go in
+// another pass over the block's weights), so the choice is speed alone.
+//
+// Grouped, by the rows an expert is expected to hold (the map itself is only
+// known on the device).  Measured on gate/up of 256 experts of 2048 x 1024, us:
+//   rows          <= 4   16    32    64   128   512
+//   tokens         128  512  1024  2048  4096  16384
+//   stream          82  151   184
+//   32 x 128        84  107   140   209   293   894
+//   64 x 256        84  108   115   155   200   537
+//   128 x 128       95  123   129   141   189   502
+//   256 x 256      104  132   139   154   202   437
+template <bool GATHER, bool SWIGLU>
+hipError_t launch_grouped(const Q8Args& a, int rows_per_block, int blocks, hipStream_t s) {
+  if (rows_per_block <= 4)
+    launch_stream<4, 2, 1, true, GATHER, SWIGLU>(a, blocks, s);
+  else if (rows_per_block <= 24)
+    launch_tile<1, 2, 1, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
+  else if (rows_per_block <= 48)
+    launch_tile<1, 4, 2, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
+  else if (rows_per_block <= 128)
+    launch_tile<2, 2, 2, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
+  else
+    launch_tile<2, 4, 4, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
+  return hipGetLastError();
+}
+
+// Dense: few rows stream the weights, with narrower workgroups where there are
+// few columns (1 x 2048 x 2048: 16 columns a workgroup 3.3 us, 32 columns 4.1);
+// else the largest tile that still gives every CU (256) a workgroup, and below
+// that the smallest tile, with four buffers in flight where even those are few.
+// Measured at K = 2048, us:        64x8192  333x2048  333x8192  1000x8192  2048x2048
+//   64 x 64, four buffers              8.5       8.4      18.1       40.0       20.7
+//   64 x 64, two buffers              11.1      10.3      14.2       32.8       17.2
+//   128 x 128                         11.6      11.4      14.9       23.0       15.9
+// and 16384x8192: 256 x 256 333, 128 x 128 447.
+hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
+  const auto tiles = [&](int bm, int bn) { return static_cast<long long>(cdiv(a.rows, bm)) * cdiv(a.N, bn); };
+  if (a.rows <= 16) {
+    if (a.N <= 32 * 256)
+      launch_stream<4, 1, 1, false, false, false>(a, 1, s);
     else
-      launch_tile<2, 4, 4, 2, GROUPED, GATHER, SWIGLU>(a, blocks, s);
+      launch_stream<4, 2, 1, false, false, false>(a, 1, s);
+  } else if (a.rows <= 32) {
+    launch_stream<4, 2, 2, false, false, false>(a, 1, s);
+  } else if (tiles(256, 256) >= 256) {
+    launch_tile<2, 4, 4, 2, 2, false, false, false>(a, cdiv(a.rows, 256), s);
+  } else if (tiles(128, 128) >= 256) {
+    launch_tile<2, 2, 2, 2, 2, false, false, false>(a, cdiv(a.rows, 128), s);
+  } else if (tiles(64, 64) > 512) {
+    launch_tile<2, 2, 1, 1, 2, false, false, false>(a, cdiv(a.rows, 64), s);
   } else {
-    if (static_cast<long long>(cdiv(a.rows, 256)) * cdiv(a.N, 256) >= 256)
-      launch_tile<2, 4, 4, 2, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 256), s);
-    else
-      launch_tile<2, 2, 2, 2, GROUPED, GATHER, SWIGLU>(a, cdiv(a.rows, 128), s);
+    launch_tile<2, 2, 1, 1, 4, false, false, false>(a, cdiv(a.rows, 64), s);
   }
   return hipGetLastError();
 }
 
-// What a grouped call expects of its block map, from the host's side alone:
-// the routed slots spread evenly over the experts they can touch.
-void expected_blocks(const moe_dims& d, int& rows_per_block, int& used) {
-  const long long S = static_cast<long long>(d.T) * d.k;
-  const int touched = static_cast<int>(S < d.E ? S : d.E);
-  const int avg = static_cast<int>((S + touched - 1) / touched);
-  const int cuts = cdiv(avg, d.tile_m_max);
-  rows_per_block = cdiv(avg, cuts);
-  used = touched * cuts + (d.n_shared ? cdiv(d.T, d.tile_m_max) : 0);
+// Rows a block is expected to hold: the routed slots spread evenly over the
+// experts, each expert's rows cut as moe_route cuts them.
+int expected_rows(const moe_dims& d) {
+  const int avg = cdiv(d.T * d.k, d.E);
+  return cdiv(avg, cdiv(avg, d.tile_m_max));
 }
 
 int validate_grouped(const moe_dims* d, const moe_route_out* r, const void* xq, const void* xs,
@@ -645,7 +698,7 @@ int moe_q8_matmul(const moe_q8_dims* d, const int8_t* xq, const float* xs, const
   a.K = d->K;
   a.type = d->type;
   (void)hipGetLastError();
-  return launched(launch_q8<false, false, false>(a, d->M, 1, 1, static_cast<hipStream_t>(stream)));
+  return launched(launch_dense(a, static_cast<hipStream_t>(stream)));
 }
 
 int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const moe_route_out* r,
@@ -664,10 +717,8 @@ int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const m
   a.ws_shared = d->n_shared ? shared->gu_s : nullptr;
   a.N = 2 * d->I;
   a.K = d->H;
-  int per, used;
-  expected_blocks(*d, per, used);
   (void)hipGetLastError();
-  return launched(launch_q8<true, true, true>(a, per, a.max_blocks, used, static_cast<hipStream_t>(stream)));
+  return launched(launch_grouped<true, true>(a, expected_rows(*d), a.max_blocks, static_cast<hipStream_t>(stream)));
 }
 
 int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* routed,
@@ -687,10 +738,8 @@ int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* ro
   a.ws_shared = d->n_shared ? shared->dn_s : nullptr;
   a.N = d->H;
   a.K = d->I;
-  int per, used;
-  expected_blocks(*d, per, used);
   (void)hipGetLastError();
-  return launched(launch_q8<true, false, false>(a, per, a.max_blocks, used, static_cast<hipStream_t>(stream)));
+  return launched(launch_grouped<false, false>(a, expected_rows(*d), a.max_blocks, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -81,10 +81,11 @@ class MoeError(RuntimeError):
 
 
 _lib = None
+_torch = None   # set with _lib
 
 
 def lib():
-    global _lib
+    global _lib, _torch
     if _lib is None:
         # torch ships its own HIP runtime.  Import it first so that loading the
         # library resolves libamdhip64.so.7 to that same runtime; loading the
@@ -164,7 +165,7 @@ def lib():
         L.moe_combine_rows_backward.restype = ctypes.c_int
         L.moe_combine_rows_backward.argtypes = [P(Dims), i32, vp, vp, P(RouteOut), vp, vp, vp]
         ELEM.update({torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.float16: ELEM_F16})
-        _lib = L
+        _lib, _torch = L, torch
     return _lib
 
 
@@ -186,10 +187,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _device() -> int:
+    """The current GPU."""
+    return _torch.cuda.current_device()
+
+
+def _stream(stream, device=None):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a stream object costs more than a small launch
+        return _torch._C._cuda_getCurrentRawStream(_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -311,19 +317,16 @@ def gdn_scan_chunked(d: GdnDims, q, k, v, g, beta, state_in, state_out, o, ws, w
 _ELEM_SIZE = (4, 2, 2)
 
 
-def _arg(t, nbytes: int, what: str):
-    """Address of a dense device array of at least nbytes (None -> NULL; raw addresses pass).
+def _arg(t, nbytes: int, what: str, device: int):
+    """Address of a dense array of at least nbytes on `device` (None -> NULL; raw addresses pass).
 
     The C side cannot see sizes or strides, so tensors that are strided, too
     small or off the current device are refused here."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: the tensor is on {t.device}, not on the current GPU")
-    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{what}: a contiguous tensor of at least {nbytes} bytes is needed, got "
-                         f"{tuple(t.shape)} {t.dtype} with strides {t.stride()}")
+    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: a contiguous tensor of at least {nbytes} bytes on GPU {device} is needed, got "
+                         f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
@@ -333,12 +336,13 @@ def _elem_bytes(elem: int) -> int:
 
 def moe_add_rmsnorm(d: NormDims, x, res, weight, sum, y, yq=None, ys=None, stream=None):
     """Residual addition and RMS norm (any of res, sum, y, yq with ys may be None)."""
+    dev = _device()
     n = d.T * d.H
     row = n * _elem_bytes(d.type)
-    _check(lib().moe_add_rmsnorm(ctypes.byref(d), _arg(x, row, "x"), _arg(res, row, "res"),
-                                 _arg(weight, 4 * d.H, "weight"), _arg(sum, row, "sum"),
-                                 _arg(y, row, "y"), _arg(yq, n, "yq"), _arg(ys, 4 * d.T, "ys"),
-                                 _stream(stream)), "moe_add_rmsnorm")
+    _check(lib().moe_add_rmsnorm(ctypes.byref(d), _arg(x, row, "x", dev), _arg(res, row, "res", dev),
+                                 _arg(weight, 4 * d.H, "weight", dev), _arg(sum, row, "sum", dev),
+                                 _arg(y, row, "y", dev), _arg(yq, n, "yq", dev), _arg(ys, 4 * d.T, "ys", dev),
+                                 _stream(stream, dev)), "moe_add_rmsnorm")
 
 
 def moe_add_rmsnorm_backward_ws_bytes(d: NormDims) -> int:
@@ -348,26 +352,29 @@ def moe_add_rmsnorm_backward_ws_bytes(d: NormDims) -> int:
 def moe_add_rmsnorm_backward(d: NormDims, sum, weight, dy, dsum, dx, dweight, ws, ws_bytes: int,
                              stream=None):
     """Gradients of moe_add_rmsnorm (dsum and dweight may be None)."""
+    dev = _device()
     row = d.T * d.H * _elem_bytes(d.type)
     _check(lib().moe_add_rmsnorm_backward(
-        ctypes.byref(d), _arg(sum, row, "sum"), _arg(weight, 4 * d.H, "weight"), _arg(dy, row, "dy"),
-        _arg(dsum, row, "dsum"), _arg(dx, row, "dx"), _arg(dweight, 4 * d.H, "dweight"),
-        _arg(ws, ws_bytes, "ws"), ws_bytes, _stream(stream)), "moe_add_rmsnorm_backward")
+        ctypes.byref(d), _arg(sum, row, "sum", dev), _arg(weight, 4 * d.H, "weight", dev), _arg(dy, row, "dy", dev),
+        _arg(dsum, row, "dsum", dev), _arg(dx, row, "dx", dev), _arg(dweight, 4 * d.H, "dweight", dev),
+        _arg(ws, ws_bytes, "ws", dev), ws_bytes, _stream(stream, dev)), "moe_add_rmsnorm_backward")
 
 
 def moe_q8_quantize(d: NormDims, x, xq, xs, stream=None):
     """Rows to int8 with a scale per row."""
+    dev = _device()
     n = d.T * d.H
-    _check(lib().moe_q8_quantize(ctypes.byref(d), _arg(x, n * _elem_bytes(d.type), "x"),
-                                 _arg(xq, n, "xq"), _arg(xs, 4 * d.T, "xs"), _stream(stream)),
+    _check(lib().moe_q8_quantize(ctypes.byref(d), _arg(x, n * _elem_bytes(d.type), "x", dev),
+                                 _arg(xq, n, "xq", dev), _arg(xs, 4 * d.T, "xs", dev), _stream(stream, dev)),
            "moe_q8_quantize")
 
 
 def moe_q8_matmul(d: Q8Dims, xq, xs, wq, ws, out, stream=None):
     """Dense product of 8-bit integers with token and channel scales."""
-    _check(lib().moe_q8_matmul(ctypes.byref(d), _arg(xq, d.M * d.K, "xq"), _arg(xs, 4 * d.M, "xs"),
-                               _arg(wq, d.N * d.K, "wq"), _arg(ws, 4 * d.N, "ws"),
-                               _arg(out, d.M * d.N * _elem_bytes(d.type), "out"), _stream(stream)),
+    dev = _device()
+    _check(lib().moe_q8_matmul(ctypes.byref(d), _arg(xq, d.M * d.K, "xq", dev), _arg(xs, 4 * d.M, "xs", dev),
+                               _arg(wq, d.N * d.K, "wq", dev), _arg(ws, 4 * d.N, "ws", dev),
+                               _arg(out, d.M * d.N * _elem_bytes(d.type), "out", dev), _stream(stream, dev)),
            "moe_q8_matmul")
 
 
@@ -376,54 +383,60 @@ def _rows_of(d: Dims) -> int:
 
 
 def moe_q8_gate_up(d: Dims, xq, xs, out: RouteOut, routed: Q8Bank, shared, h, stream=None):
-    _check(lib().moe_q8_gate_up(ctypes.byref(d), _arg(xq, d.T * d.H, "xq"), _arg(xs, 4 * d.T, "xs"),
+    dev = _device()
+    _check(lib().moe_q8_gate_up(ctypes.byref(d), _arg(xq, d.T * d.H, "xq", dev), _arg(xs, 4 * d.T, "xs", dev),
                                 ctypes.byref(out), ctypes.byref(routed),
                                 ctypes.byref(shared) if shared is not None else None,
-                                _arg(h, 2 * _rows_of(d) * d.I, "h"), _stream(stream)),
+                                _arg(h, 2 * _rows_of(d) * d.I, "h", dev), _stream(stream, dev)),
            "moe_q8_gate_up")
 
 
 def moe_q8_down(d: Dims, out: RouteOut, routed: Q8Bank, shared, hq, hs, y_slots, stream=None):
+    dev = _device()
     rows = _rows_of(d)
     _check(lib().moe_q8_down(ctypes.byref(d), ctypes.byref(out), ctypes.byref(routed),
                              ctypes.byref(shared) if shared is not None else None,
-                             _arg(hq, rows * d.I, "hq"), _arg(hs, 4 * rows, "hs"),
-                             _arg(y_slots, 2 * rows * d.H, "y_slots"), _stream(stream)),
+                             _arg(hq, rows * d.I, "hq", dev), _arg(hs, 4 * rows, "hs", dev),
+                             _arg(y_slots, 2 * rows * d.H, "y_slots", dev), _stream(stream, dev)),
            "moe_q8_down")
 
 
 def moe_dispatch_rows(d: Dims, elem: int, x, out: RouteOut, rows, stream=None):
     """Token rows into moe_route's order (elem: one of ELEM_*)."""
+    dev = _device()
     e = _elem_bytes(elem) * d.H
-    _check(lib().moe_dispatch_rows(ctypes.byref(d), elem, _arg(x, d.T * e, "x"), ctypes.byref(out),
-                                   _arg(rows, _rows_of(d) * e, "rows"), _stream(stream)),
+    _check(lib().moe_dispatch_rows(ctypes.byref(d), elem, _arg(x, d.T * e, "x", dev), ctypes.byref(out),
+                                   _arg(rows, _rows_of(d) * e, "rows", dev), _stream(stream, dev)),
            "moe_dispatch_rows")
 
 
 def moe_dispatch_rows_backward(d: Dims, elem: int, drows, out: RouteOut, dx, stream=None):
+    dev = _device()
     e = _elem_bytes(elem) * d.H
-    _check(lib().moe_dispatch_rows_backward(ctypes.byref(d), elem, _arg(drows, _rows_of(d) * e, "drows"),
-                                            ctypes.byref(out), _arg(dx, d.T * e, "dx"),
-                                            _stream(stream)), "moe_dispatch_rows_backward")
+    _check(lib().moe_dispatch_rows_backward(ctypes.byref(d), elem, _arg(drows, _rows_of(d) * e, "drows", dev),
+                                            ctypes.byref(out), _arg(dx, d.T * e, "dx", dev),
+                                            _stream(stream, dev)), "moe_dispatch_rows_backward")
 
 
 def moe_combine_rows(d: Dims, elem: int, rows, out: RouteOut, y, stream=None):
     """moe_combine for any row type."""
+    dev = _device()
     e = _elem_bytes(elem) * d.H
-    _check(lib().moe_combine_rows(ctypes.byref(d), elem, _arg(rows, _rows_of(d) * e, "rows"),
-                                  ctypes.byref(out), _arg(y, d.T * e, "y"), _stream(stream)),
+    _check(lib().moe_combine_rows(ctypes.byref(d), elem, _arg(rows, _rows_of(d) * e, "rows", dev),
+                                  ctypes.byref(out), _arg(y, d.T * e, "y", dev), _stream(stream, dev)),
            "moe_combine_rows")
 
 
 def moe_combine_rows_backward(d: Dims, elem: int, dy, rows, out: RouteOut, drows, dtopk_w,
                               stream=None):
     """Gradients of the combine (dtopk_w None: rows is not read and may be None)."""
+    dev = _device()
     e = _elem_bytes(elem) * d.H
-    _check(lib().moe_combine_rows_backward(ctypes.byref(d), elem, _arg(dy, d.T * e, "dy"),
-                                           _arg(rows, _rows_of(d) * e, "rows"), ctypes.byref(out),
-                                           _arg(drows, _rows_of(d) * e, "drows"),
-                                           _arg(dtopk_w, 4 * d.T * d.k, "dtopk_w"),
-                                           _stream(stream)), "moe_combine_rows_backward")
+    _check(lib().moe_combine_rows_backward(ctypes.byref(d), elem, _arg(dy, d.T * e, "dy", dev),
+                                           _arg(rows, _rows_of(d) * e, "rows", dev), ctypes.byref(out),
+                                           _arg(drows, _rows_of(d) * e, "drows", dev),
+                                           _arg(dtopk_w, 4 * d.T * d.k, "dtopk_w", dev),
+                                           _stream(stream, dev)), "moe_combine_rows_backward")
 
 
 # --------------------------------------------------------------------- device buffers
