@@ -82,6 +82,30 @@ struct Elem<MOE_ELEM_F16> {
 };
 
 // ---------------------------------------------------------------------------
+// Streaming accesses: NT marks data that is not used again before it would be
+// evicted anyway, so that it does not push out what is.  An array larger than
+// the L2s together (8 x 4 MB) leaves them before a later kernel reads it; one
+// larger than a quarter of the 256 MB last-level cache does not stay there
+// next to the other arrays of a step.
+// ---------------------------------------------------------------------------
+constexpr size_t kStreamStore = 32u << 20;
+constexpr size_t kStreamLoad = 64u << 20;
+
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  if (!NT) return *p;
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <bool NT>
+__device__ __forceinline__ void store16(uint4* p, uint4 v) {
+  if (!NT)
+    *p = v;
+  else
+    __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
+
+// ---------------------------------------------------------------------------
 // Reductions over a wave of 64, every lane gets the result: four steps inside
 // the 16-lane DPP rows (pairs, quads, halves of eight, the row), then the rows
 // against each other with the two swap instructions.  The order is fixed.

@@ -30,12 +30,12 @@ struct Raw8 {
   uint4 q[8 / Elem<TYPE>::V];
 };
 
-template <int TYPE>
+template <int TYPE, bool NT>
 __device__ __forceinline__ Raw8<TYPE> load8(const void* base, size_t chunk) {
   constexpr int n = 8 / Elem<TYPE>::V;
   Raw8<TYPE> r;
 #pragma unroll
-  for (int i = 0; i < n; ++i) r.q[i] = static_cast<const uint4*>(base)[chunk * n + i];
+  for (int i = 0; i < n; ++i) r.q[i] = load16<NT>(static_cast<const uint4*>(base) + chunk * n + i);
   return r;
 }
 
@@ -45,12 +45,12 @@ __device__ __forceinline__ void unpack8(const Raw8<TYPE>& r, float (&v)[8]) {
   for (int i = 0; i < 8 / Elem<TYPE>::V; ++i) Elem<TYPE>::unpack(r.q[i], v + i * Elem<TYPE>::V);
 }
 
-template <int TYPE>
+template <int TYPE, bool NT>
 __device__ __forceinline__ void store8(void* base, size_t chunk, const float (&v)[8]) {
   constexpr int n = 8 / Elem<TYPE>::V;
 #pragma unroll
   for (int i = 0; i < n; ++i)
-    static_cast<uint4*>(base)[chunk * n + i] = Elem<TYPE>::pack(v + i * Elem<TYPE>::V);
+    store16<NT>(static_cast<uint4*>(base) + chunk * n + i, Elem<TYPE>::pack(v + i * Elem<TYPE>::V));
 }
 
 __device__ __forceinline__ void load_weight8(const float* w, int chunk, float (&v)[8]) {
@@ -117,7 +117,7 @@ __device__ __forceinline__ uint32_t quant4(const float* y, const RowScale& r) {
 }
 
 // NORM false: the 8-bit form of x alone (y = x).
-template <int TYPE, int NW, int C, bool NORM>
+template <int TYPE, int NW, int C, bool NORM, bool NT>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void add_rmsnorm_kernel(
     int T, int H, float eps, const void* x, const void* res, const float* __restrict__ weight,
     void* sum, void* y, int8_t* __restrict__ yq, float* __restrict__ ys) {
@@ -137,8 +137,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void add_rmsnorm_kernel(
     for (int i = 0; i < C; ++i) {
       const int c = li + i * 64 * NW;
       if (c < chunks) {
-        a[i] = load8<TYPE>(x, base + c);
-        if (NORM && res) b[i] = load8<TYPE>(res, base + c);
+        a[i] = load8<TYPE, NT>(x, base + c);
+        if (NORM && res) b[i] = load8<TYPE, NT>(res, base + c);
       }
     }
     if (NORM) {
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void add_rmsnorm_kernel(
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int c = li + i * 64 * NW;
-        if (c < chunks) store8<TYPE>(sum, base + c, v[i]);
+        if (c < chunks) store8<TYPE, NT>(sum, base + c, v[i]);
       }
     }
     ss = row_sum<NW>(ss, red_s, wave);
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void add_rmsnorm_kernel(
       if (c < chunks) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rho * w[i][e];
-        if (y) store8<TYPE>(y, base + c, v[i]);
+        if (y) store8<TYPE, NT>(y, base + c, v[i]);
       }
     }
     if (!yq) return;
@@ -221,7 +221,7 @@ constexpr int kBwdWaves = 8;  // waves per workgroup where a wave holds a row
 template <int NW>
 constexpr int bwd_threads() { return NW == 1 ? 64 * kBwdWaves : 64 * NW; }
 
-template <int TYPE, int NW, int C>
+template <int TYPE, int NW, int C, bool NT>
 __global__ __launch_bounds__(bwd_threads<NW>()) void add_rmsnorm_backward_kernel(
     int T, int H, float eps, const void* __restrict__ sum, const float* __restrict__ weight,
     const void* dy, const void* dsum, void* dx, float* __restrict__ part) {
@@ -255,9 +255,9 @@ __global__ __launch_bounds__(bwd_threads<NW>()) void add_rmsnorm_backward_kernel
     for (int i = 0; i < C; ++i) {
       const int c = li + i * 64 * NW;
       if (c < chunks) {
-        rs[i] = load8<TYPE>(sum, base + c);
-        rd[i] = load8<TYPE>(dy, base + c);
-        if (dsum) rr[i] = load8<TYPE>(dsum, base + c);
+        rs[i] = load8<TYPE, NT>(sum, base + c);
+        rd[i] = load8<TYPE, NT>(dy, base + c);
+        if (dsum) rr[i] = load8<TYPE, NT>(dsum, base + c);
       } else {
 #pragma unroll
         for (int q = 0; q < 8 / Elem<TYPE>::V; ++q) rs[i].q[q] = rd[i].q[q] = make_uint4(0, 0, 0, 0);
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(bwd_threads<NW>()) void add_rmsnorm_backward_kernel
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += u[e];
         }
-        store8<TYPE>(dx, base + c, o);
+        store8<TYPE, NT>(dx, base + c, o);
       }
     }
   }
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(int P, int H, const 
   const int c = blockIdx.x * 64 + lane;
   float t = 0.0f;
   if (c < H) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = wave; p < P; p += 16) t += part[static_cast<size_t>(p) * H + c];
   }
   red[wave][lane] = t;
@@ -383,10 +383,18 @@ int validate_norm(const moe_norm_dims* d) {
 }
 
 // Waves per row: one where the row fits a wave (H <= 2048) and there are rows
-// enough to fill the chip, else four (H <= 8192), else sixteen.
+// enough to fill the chip, else four (H <= 8192), else sixteen.  At 2048 x 2048
+// the forward pass takes the same either way; the gradient of 333 x 2048 takes
+// 10.1 us with one wave a row and 8.3 with four, of 4096 x 2048 17.1 with one.
 int row_waves(int T, int H) {
   if (H <= 2048 && T >= 2048) return 1;
   return H <= 8192 ? 4 : 16;
+}
+
+// Rows that leave the L2s before anyone reads them again go past the caches
+// (16384 x 4096 with 8 bits: 109 us -> 99; gradient of 16384 x 2048: 57 -> 53).
+bool streamed(const moe_norm_dims& d) {
+  return static_cast<size_t>(d.T) * d.H * elem_bytes(d.type) > kStreamStore;
 }
 
 template <int TYPE, int NW, int C, bool NORM>
@@ -394,7 +402,8 @@ void launch_norm(const moe_norm_dims& d, const void* x, const void* res, const f
                  void* sum, void* y, int8_t* yq, float* ys, hipStream_t stream) {
   const int rows = NW == 1 ? 4 : 1;
   const unsigned groups = static_cast<unsigned>((d.T + rows - 1) / rows);
-  hipLaunchKernelGGL((add_rmsnorm_kernel<TYPE, NW, C, NORM>),
+  hipLaunchKernelGGL((streamed(d) ? add_rmsnorm_kernel<TYPE, NW, C, NORM, true>
+                                  : add_rmsnorm_kernel<TYPE, NW, C, NORM, false>),
                      dim3(groups < kGridX ? groups : kGridX, (groups + kGridX - 1) / kGridX),
                      dim3(NW == 1 ? 256 : 64 * NW), 0, stream, d.T, d.H, d.eps, x, res, weight, sum,
                      y, yq, ys);
@@ -428,12 +437,15 @@ hipError_t launch_norm_any(const moe_norm_dims& d, const void* x, const void* re
   return hipGetLastError();
 }
 
-// Workgroups of the gradient kernel: enough to hold every wave slot a few
-// times over, few enough that the partial sums stay small next to the rows.
+// Workgroups of the gradient kernel: one per CU of eight waves, two of four
+// waves once there are rows for both, one of sixteen.  More of them hide more
+// latency but leave more partial sums to add.  Measured, us: 16384 x 2048 256
+// groups 50.7, 512 53; 333 x 2048 256 8.3, 512 9.5; 2000 x 2048 256 16.2, 512
+// 12.8, 1024 14.4; 2048 x 16384 128 69, 256 56, 512 64.
 int bwd_groups(const moe_norm_dims& d) {
   const int nw = row_waves(d.T, d.H);
   const int rows = nw == 1 ? kBwdWaves : 1;
-  const int cap = nw == 4 ? 1024 : 512;
+  const int cap = nw == 4 && d.T >= 1024 ? 512 : 256;
   const int need = (d.T + rows - 1) / rows;
   return need < cap ? need : cap;
 }
@@ -445,8 +457,9 @@ void launch_bwd_type(const moe_norm_dims& d, const void* sum, const float* weigh
   const int c = (d.H / 8 + 64 * nw - 1) / (64 * nw);
   const dim3 grid(static_cast<unsigned>(bwd_groups(d)));
 #define MOE_BWD(NW, C)                                                                           \
-  hipLaunchKernelGGL((add_rmsnorm_backward_kernel<TYPE, NW, C>), grid, dim3(bwd_threads<NW>()), 0, \
-                     s, d.T, d.H, d.eps, sum, weight, dy, dsum, dx, part)
+  hipLaunchKernelGGL((streamed(d) ? add_rmsnorm_backward_kernel<TYPE, NW, C, true>               \
+                                  : add_rmsnorm_backward_kernel<TYPE, NW, C, false>),            \
+                     grid, dim3(bwd_threads<NW>()), 0, s, d.T, d.H, d.eps, sum, weight, dy, dsum, dx, part)
   if (nw == 1) {
     if (c == 1) MOE_BWD(1, 1); else if (c == 2) MOE_BWD(1, 2); else if (c == 3) MOE_BWD(1, 3); else MOE_BWD(1, 4);
   } else if (nw == 4) {

@@ -12,7 +12,12 @@
 // its gradient) is then read or written once and its k+1 sorted rows are each
 // touched by one workgroup, so there is nothing to add up across workgroups,
 // no atomics, and every sorted row is still one contiguous run of whole
-// 16-byte accesses.  Slot positions and weights are workgroup-uniform.
+// 16-byte accesses.  Slot positions and weights are workgroup-uniform.  Sorted
+// rows of large batches are streamed past the caches (kStreamStore, kStreamLoad
+// in block.h).  Measured at 8192 tokens of 2048 bfloat16, 8 + 1 rows a token
+// (335 MB moved, 637 MB for the combine's gradient), us plain -> streamed:
+// dispatch 68 -> 53, combine 65 -> 57, its gradient 123 -> 108, the dispatch's
+// 65 -> 57: 5.9 to 6.3 TB/s, the rate of a plain streaming read (5.85).
 #include "block.h"
 
 namespace moe {
@@ -40,6 +45,7 @@ __device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ slot_pos
 }
 
 // chunks: 16-byte pieces of a row.  One token and 256 pieces per workgroup.
+template <bool NT>
 __global__ __launch_bounds__(kRowThreads) void dispatch_rows_kernel(
     int T, int k, int n_shared, int chunks, const int32_t* __restrict__ slot_pos,
     const uint4* __restrict__ x, uint4* __restrict__ rows, uint32_t* __restrict__ status) {
@@ -52,13 +58,13 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_rows_kernel(
     const Slots s = load_slots(slot_pos, t, k, S, j0, status);
 #pragma unroll
     for (int u = 0; u < kGroup; ++u)
-      if (s.ok[u]) rows[static_cast<size_t>(s.pos[u]) * chunks + c] = v;
+      if (s.ok[u]) store16<NT>(rows + static_cast<size_t>(s.pos[u]) * chunks + c, v);
   }
-  if (n_shared) rows[(static_cast<size_t>(S) + t) * chunks + c] = v;
+  if (n_shared) store16<NT>(rows + (static_cast<size_t>(S) + t) * chunks + c, v);
 }
 
 // WEIGHTED: the combine; else the gradient of the dispatch (weights of one).
-template <int TYPE, bool WEIGHTED>
+template <int TYPE, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
     int T, int k, int n_shared, int chunks, const float* __restrict__ topk_w,
     const int32_t* __restrict__ slot_pos, const uint4* __restrict__ rows, uint4* __restrict__ y,
@@ -68,7 +74,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
   const int c = static_cast<int>(blockIdx.y) * kRowThreads + threadIdx.x;
   if (c >= chunks) return;
   const int S = T * k;
-  const uint4 vsh = rows[static_cast<size_t>(n_shared ? S + t : 0) * chunks + c];
+  const uint4 vsh = load16<NT>(rows + static_cast<size_t>(n_shared ? S + t : 0) * chunks + c);
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.0f;
@@ -78,7 +84,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
     float w[kGroup];
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
-      v[u] = rows[static_cast<size_t>(s.pos[u]) * chunks + c];
+      v[u] = load16<NT>(rows + static_cast<size_t>(s.pos[u]) * chunks + c);
       w[u] = WEIGHTED ? topk_w[static_cast<size_t>(t) * k + min(j0 + u, k - 1)] : 1.0f;
     }
 #pragma unroll
@@ -101,7 +107,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
 
 // One token per workgroup: dy's pieces are scaled into the k+1 rows, and the k
 // dot products are summed over the workgroup (lanes, then the four waves).
-template <int TYPE>
+template <int TYPE, bool NTL, bool NTS>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_backward_kernel(
     int T, int k, int n_shared, int chunks, const float* __restrict__ topk_w,
     const int32_t* __restrict__ slot_pos, const uint4* __restrict__ dy, const uint4* rows,
@@ -124,11 +130,11 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_backward_kernel(
       uint4 v[kGroup];
       if (dw) {
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) v[u] = rows[static_cast<size_t>(s.pos[u]) * chunks + c];
+        for (int u = 0; u < kGroup; ++u) v[u] = load16<NTL>(rows + static_cast<size_t>(s.pos[u]) * chunks + c);
       }
       float d[V];
       Elem<TYPE>::unpack(draw, d);
-      if (j0 == 0 && n_shared) drows[(static_cast<size_t>(S) + t) * chunks + c] = draw;
+      if (j0 == 0 && n_shared) store16<NTS>(drows + (static_cast<size_t>(S) + t) * chunks + c, draw);
 #pragma unroll
       for (int u = 0; u < kGroup; ++u) {
         if (!s.ok[u]) continue;
@@ -141,7 +147,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_backward_kernel(
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = w[u] * d[e];
-        drows[static_cast<size_t>(s.pos[u]) * chunks + c] = Elem<TYPE>::pack(o);
+        store16<NTS>(drows + static_cast<size_t>(s.pos[u]) * chunks + c, Elem<TYPE>::pack(o));
       }
     }
     if (dw) {
@@ -173,6 +179,11 @@ int validate_rows(const moe_dims* d, int32_t type, const moe_route_out* r, bool 
 
 int row_chunks(const moe_dims& d, int type) { return d.H * elem_bytes(type) / 16; }
 
+// Bytes of the sorted rows.
+size_t rows_bytes(const moe_dims& d, int type) {
+  return static_cast<size_t>(d.T) * (d.k + d.n_shared) * d.H * elem_bytes(type);
+}
+
 template <bool WEIGHTED>
 int combine_any(const moe_dims& d, int type, const void* rows, const moe_route_out* r, void* y,
                 void* stream) {
@@ -180,10 +191,12 @@ int combine_any(const moe_dims& d, int type, const void* rows, const moe_route_o
   const dim3 grid(static_cast<unsigned>(d.T), static_cast<unsigned>((chunks + kRowThreads - 1) / kRowThreads));
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
+  const bool stream_rows = rows_bytes(d, type) > kStreamLoad;
 #define MOE_COMBINE(TYPE)                                                                        \
-  hipLaunchKernelGGL((combine_rows_kernel<TYPE, WEIGHTED>), grid, dim3(kRowThreads), 0, s, d.T,  \
-                     d.k, d.n_shared, chunks, r->topk_w, r->slot_pos,                            \
-                     static_cast<const uint4*>(rows), static_cast<uint4*>(y), r->status)
+  hipLaunchKernelGGL((stream_rows ? combine_rows_kernel<TYPE, WEIGHTED, true>                    \
+                                  : combine_rows_kernel<TYPE, WEIGHTED, false>),                 \
+                     grid, dim3(kRowThreads), 0, s, d.T, d.k, d.n_shared, chunks, r->topk_w,     \
+                     r->slot_pos, static_cast<const uint4*>(rows), static_cast<uint4*>(y), r->status)
   switch (type) {
     case MOE_ELEM_F32: MOE_COMBINE(MOE_ELEM_F32); break;
     case MOE_ELEM_BF16: MOE_COMBINE(MOE_ELEM_BF16); break;
@@ -211,8 +224,9 @@ int moe_dispatch_rows(const moe_dims* d, int32_t type, const void* x, const moe_
   const int chunks = row_chunks(*d, type);
   const dim3 grid(static_cast<unsigned>(d->T), static_cast<unsigned>((chunks + kRowThreads - 1) / kRowThreads));
   (void)hipGetLastError();
-  hipLaunchKernelGGL(dispatch_rows_kernel, grid, dim3(kRowThreads), 0,
-                     static_cast<hipStream_t>(stream), d->T, d->k, d->n_shared, chunks, r->slot_pos,
+  hipLaunchKernelGGL((rows_bytes(*d, type) > kStreamStore ? dispatch_rows_kernel<true>
+                                                          : dispatch_rows_kernel<false>),
+                     grid, dim3(kRowThreads), 0, static_cast<hipStream_t>(stream), d->T, d->k, d->n_shared, chunks, r->slot_pos,
                      static_cast<const uint4*>(x), static_cast<uint4*>(rows), r->status);
   return launched(hipGetLastError());
 }
@@ -252,10 +266,13 @@ int moe_combine_rows_backward(const moe_dims* d, int32_t type, const void* dy, c
   const dim3 grid(static_cast<unsigned>(d->T));
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
+  const size_t bytes = rows_bytes(*d, type);
 #define MOE_COMBINE_BWD(TYPE)                                                                    \
-  hipLaunchKernelGGL((combine_rows_backward_kernel<TYPE>), grid, dim3(kRowThreads), 0, s, d->T,  \
-                     d->k, d->n_shared, chunks, r->topk_w, r->slot_pos,                          \
-                     static_cast<const uint4*>(dy), static_cast<const uint4*>(rows),             \
+  hipLaunchKernelGGL((bytes > kStreamLoad    ? combine_rows_backward_kernel<TYPE, true, true>    \
+                      : bytes > kStreamStore ? combine_rows_backward_kernel<TYPE, false, true>   \
+                                             : combine_rows_backward_kernel<TYPE, false, false>), \
+                     grid, dim3(kRowThreads), 0, s, d->T, d->k, d->n_shared, chunks, r->topk_w,  \
+                     r->slot_pos, static_cast<const uint4*>(dy), static_cast<const uint4*>(rows), \
                      static_cast<uint4*>(drows), dtopk_w, r->status)
   switch (type) {
     case MOE_ELEM_F32: MOE_COMBINE_BWD(MOE_ELEM_F32); break;
