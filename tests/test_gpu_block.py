@@ -370,6 +370,10 @@ EXPERT_SIZES = [(1, 64, 64, 4, 1, 0, 16, 16), (1, 2048, 512, 256, 8, 1, 32, 16),
                 (16, 256, 128, 8, 2, 1, 128, 16), (37, 320, 64, 300, 8, 0, 32, 32), (100, 192, 320, 6, 3, 1, 256, 16),
                 (200, 128, 128, 3, 2, 1, 48, 16), (600, 64, 192, 4, 2, 1, 128, 16), (513, 576, 128, 9, 4, 0, 64, 32),
                 (1500, 128, 64, 5, 2, 1, 256, 16), (300, 128, 64, 1, 1, 1, 240, 16), (64, 128, 64, 1024, 4, 1, 16, 16)]
+# few rows an expert, but every token in the shared one, whose blocks take several passes
+EXPERT_SIZES += [(17, 128, 64, 64, 1, 1, 64, 16), (40, 192, 64, 64, 1, 1, 64, 16), (300, 128, 128, 300, 2, 1, 256, 16),
+                 (1294, 192, 320, 105, 1, 1, 128, 16), (4096, 64, 512, 512, 1, 1, 256, 16),
+                 (8192, 64, 1024, 1024, 1, 1, 256, 32)]
 
 
 def bank(rng, n, rows, K):

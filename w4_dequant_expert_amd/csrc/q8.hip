@@ -13,6 +13,8 @@
 //     with no LDS and no barrier until the waves' sums are added.
 //   q8_tile_kernel: many rows.  Bound by the int8 matrix rate; tiles of both
 //     operands go through LDS in steps of 128 inputs.
+#include <algorithm>
+
 #include "block.h"
 
 namespace moe {
@@ -32,6 +34,8 @@ struct Q8Args {
   int rows;                 // rows of the output
   int N, K;                 // rows and inputs of one weight matrix
   int type;                 // output element
+  int stream_out;           // outputs past the caches (more of them than kStreamStore)
+  int stream_w;             // an expert's rows are one block, so its weights are read once
   // grouped products only
   const int32_t* blocks;
   const int32_t* n_blocks;
@@ -45,6 +49,7 @@ struct Q8Block {
   const int8_t* w;
   const float* ws;
   int row0, rows;
+  bool once;  // nobody else reads these weights
 };
 
 // Block b < max_blocks of the map; false past its end, and (with the status
@@ -64,6 +69,7 @@ __device__ __forceinline__ bool q8_block(const Q8Args& a, int b, Q8Block& o) {
   }
   o.w = shared ? a.w_shared : a.w + static_cast<size_t>(g) * a.N * a.K;
   o.ws = shared ? a.ws_shared : a.ws + static_cast<size_t>(g) * a.N;
+  o.once = a.stream_w && !shared;
   return true;
 }
 
@@ -152,6 +158,7 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
     blk.ws = a.ws;
     blk.row0 = 0;
     blk.rows = a.rows;
+    blk.once = false;
   }
   const int8_t* wp[CT];
 #pragma unroll
@@ -267,6 +274,7 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // in its own L2.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
+constexpr int kNonTemporal = 2;  // cache policy of a copy whose data nobody else reads
 
 // At most N of this wave's copies are still in flight, its LDS reads are done
 // and every wave is here.  The wait is the builtin, which the compiler's own bookkeeping of waits
@@ -329,9 +337,14 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
     const int r = (it * 64 + lane) / PIECES, piece = (it * 64 + lane) % PIECES;
     const uint4 v = *reinterpret_cast<const uint4*>(out + r * PIECES * 16 + ((piece ^ (r & (PIECES - 1))) << 4));
     const int c = c0 + piece * (16 / ELEM);
-    if (m1 + r < blk.rows && c < n_out && ((stored >> r) & 1))
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
-                                (static_cast<size_t>(blk.row0 + m1 + r) * n_out + c) * ELEM) = v;
+    if (m1 + r < blk.rows && c < n_out && ((stored >> r) & 1)) {
+      uint4* const to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
+                                                 (static_cast<size_t>(blk.row0 + m1 + r) * n_out + c) * ELEM);
+      if (a.stream_out)
+        store16<true>(to, v);
+      else
+        store16<false>(to, v);
+    }
   }
   asm volatile("" ::: "memory");
 }
@@ -361,9 +374,15 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
     // (read into LDS, never multiplied)
     const int at = s * kStep + t.piece;
     const int k0 = at < a.K ? at : at - 64;
+    if (GROUPED && WM * M <= 2 && blk.once) {
 #pragma unroll
-    for (int i = 0; i < WCOPY; ++i)
-      __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+      for (int i = 0; i < WCOPY; ++i)
+        __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, kNonTemporal);
+    } else {
+#pragma unroll
+      for (int i = 0; i < WCOPY; ++i)
+        __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < XC; ++i)
       __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0, 0);
@@ -527,6 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
     blk.ws = a.ws;
     blk.row0 = b * BM;
     blk.rows = min(BM, a.rows - blk.row0);
+    blk.once = false;
   }
   const int v0 = ni * BN;
   TileWave<WCOPY, XCOPY> t;
@@ -570,33 +590,9 @@ void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
                      dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
 
-// Which kernel.  Every one of them takes any block (rows past its tile go in
-// another pass over the block's weights), so the choice is speed alone.
+// Which kernel.  Every one of them takes any number of rows (those past its
+// tile in another pass over the weights), so the choice is speed alone.
 //
-// Grouped, by the rows an expert is expected to hold (the map itself is only
-// known on the device).  Measured on gate/up of 256 experts of 2048 x 1024, us:
-//   rows          <= 4   16    32    64   128   512
-//   tokens         128  512  1024  2048  4096  16384
-//   stream          82  151   184
-//   32 x 128        84  107   140   209   293   894
-//   64 x 256        84  108   115   155   200   537
-//   128 x 128       95  123   129   141   189   502
-//   256 x 256      104  132   139   154   202   437
-template <bool GATHER, bool SWIGLU>
-hipError_t launch_grouped(const Q8Args& a, int rows_per_block, int blocks, hipStream_t s) {
-  if (rows_per_block <= 4)
-    launch_stream<4, 2, 1, true, GATHER, SWIGLU>(a, blocks, s);
-  else if (rows_per_block <= 24)
-    launch_tile<1, 2, 1, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
-  else if (rows_per_block <= 48)
-    launch_tile<1, 4, 2, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
-  else if (rows_per_block <= 128)
-    launch_tile<2, 2, 2, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
-  else
-    launch_tile<2, 4, 4, 2, 2, true, GATHER, SWIGLU>(a, blocks, s);
-  return hipGetLastError();
-}
-
 // Dense: few rows stream the weights, with narrower workgroups where there are
 // few columns (1 x 2048 x 2048: 16 columns a workgroup 3.3 us, 32 columns 4.1);
 // else the largest tile that still gives every CU (256) a workgroup, and below
@@ -627,11 +623,37 @@ hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows a block is expected to hold: the routed slots spread evenly over the
-// experts, each expert's rows cut as moe_route cuts them.
-int expected_rows(const moe_dims& d) {
-  const int avg = cdiv(d.T * d.k, d.E);
-  return cdiv(avg, cdiv(avg, d.tile_m_max));
+// Grouped: the map is only known on the device, so the choice goes by the rows
+// an expert holds in the mean and by the tallest block to expect: the shared
+// expert holds every token, another expert a few times the mean, and the map
+// cuts both at tile_m_max.  A block taller than the kernel's tile takes several
+// passes and ends last; a tile much taller than the blocks holds less of the
+// weights in flight.  Measured on gate/up of 256 experts of 2048 x 1024, eight
+// each and a shared one, us by tokens/tile_m_max:
+//               128/128  256/128  512/32  512/128  1024/128  2048/128  2048/256  4096/256  16384/256
+//   stream          99      127     154      180       273       461       508       872
+//   32 x 128        93      109     103      140       184       288       324       539       894
+//   64 x 256        82       90     103      115       140       188       210       318       537
+//   128 x 128       91       98     123      106       122       145       159       216       502
+//   256 x 256      103      107     134      114       134       153       155       186       437
+// (128 tokens in blocks of at most 32: stream 82, 32 x 128 84; 512 in blocks of
+// at most 16: stream 146, 32 x 128 123.)  Weights that are
+// read once are copied past the caches (512 tokens, down: 60 us -> 57).
+template <bool GATHER, bool SWIGLU>
+hipError_t launch_grouped(const moe_dims& d, const Q8Args& a, hipStream_t s) {
+  const int mean = cdiv(d.T * d.k, d.E);
+  const int tallest = std::min(d.tile_m_max, d.n_shared ? std::max(d.T, mean) : 4 * mean);
+  if (tallest <= 16 && mean <= 4)
+    launch_stream<4, 2, 1, true, GATHER, SWIGLU>(a, a.max_blocks, s);
+  else if (tallest <= 32)
+    launch_tile<1, 2, 1, 2, 2, true, GATHER, SWIGLU>(a, a.max_blocks, s);
+  else if (tallest <= 64 || mean <= 8)
+    launch_tile<1, 4, 2, 2, 2, true, GATHER, SWIGLU>(a, a.max_blocks, s);
+  else if (tallest <= 128 || mean <= 32)
+    launch_tile<2, 2, 2, 2, 2, true, GATHER, SWIGLU>(a, a.max_blocks, s);
+  else
+    launch_tile<2, 4, 4, 2, 2, true, GATHER, SWIGLU>(a, a.max_blocks, s);
+  return hipGetLastError();
 }
 
 int validate_grouped(const moe_dims* d, const moe_route_out* r, const void* xq, const void* xs,
@@ -650,17 +672,19 @@ int validate_half(const int8_t* w, const float* s) {
 }
 
 Q8Args grouped_args(const moe_dims& d, const moe_route_out* r, const int8_t* xq, const float* xs,
-                    void* out) {
+                    void* out, int width) {
   Q8Args a{};
   a.x = xq;
   a.xs = xs;
   a.out = out;
   a.rows = d.T * (d.k + d.n_shared);
   a.type = MOE_ELEM_BF16;
+  a.stream_out = static_cast<size_t>(a.rows) * width * 2 > kStreamStore;
   a.blocks = r->blocks;
   a.n_blocks = r->n_blocks;
   a.sorted_slot = r->sorted_slot;
   a.status = r->status;
+  a.stream_w = cdiv(d.T * d.k, d.E) <= d.tile_m_max;
   a.max_blocks = max_blocks_of(d);
   a.E = d.E;
   a.T = d.T;
@@ -697,6 +721,7 @@ int moe_q8_matmul(const moe_q8_dims* d, const int8_t* xq, const float* xs, const
   a.N = d->N;
   a.K = d->K;
   a.type = d->type;
+  a.stream_out = static_cast<size_t>(d->M) * d->N * elem_bytes(d->type) > kStreamStore;
   (void)hipGetLastError();
   return launched(launch_dense(a, static_cast<hipStream_t>(stream)));
 }
@@ -710,7 +735,7 @@ int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const m
   if (d->n_shared && (rc = validate_half(shared->gu, shared->gu_s))) return rc;
   if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
-  Q8Args a = grouped_args(*d, r, xq, xs, h);
+  Q8Args a = grouped_args(*d, r, xq, xs, h, d->I);
   a.w = routed->gu;
   a.ws = routed->gu_s;
   a.w_shared = d->n_shared ? shared->gu : nullptr;
@@ -718,7 +743,7 @@ int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const m
   a.N = 2 * d->I;
   a.K = d->H;
   (void)hipGetLastError();
-  return launched(launch_grouped<true, true>(a, expected_rows(*d), a.max_blocks, static_cast<hipStream_t>(stream)));
+  return launched(launch_grouped<true, true>(*d, a, static_cast<hipStream_t>(stream)));
 }
 
 int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* routed,
@@ -731,7 +756,7 @@ int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* ro
   if (d->n_shared && (rc = validate_half(shared->dn, shared->dn_s))) return rc;
   if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
-  Q8Args a = grouped_args(*d, r, hq, hs, y_slots);
+  Q8Args a = grouped_args(*d, r, hq, hs, y_slots, d->H);
   a.w = routed->dn;
   a.ws = routed->dn_s;
   a.w_shared = d->n_shared ? shared->dn : nullptr;
@@ -739,7 +764,7 @@ int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* ro
   a.N = d->H;
   a.K = d->I;
   (void)hipGetLastError();
-  return launched(launch_grouped<false, false>(a, expected_rows(*d), a.max_blocks, static_cast<hipStream_t>(stream)));
+  return launched(launch_grouped<false, false>(*d, a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -189,7 +189,9 @@ def _ptr(t):
 
 def _device() -> int:
     """The current GPU."""
-    return _torch.cuda.current_device()
+    if not _torch.cuda.is_initialized():
+        _torch.cuda.init()
+    return _torch._C._cuda_getDevice()
 
 
 def _stream(stream, device=None):
