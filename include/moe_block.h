@@ -19,7 +19,8 @@
  * can be captured into a HIP graph; two calls may overlap as long as neither
  * writes what the other uses.  Unless an argument says otherwise, outputs may
  * not overlap inputs.  No kernel uses floating-point atomics: equal inputs
- * give equal bits.
+ * give equal bits.  A call without rows (T = 0, M = 0) enqueues nothing and
+ * looks at no array, except that moe_add_rmsnorm_backward clears dweight.
  */
 #ifndef MOE_BLOCK_H
 #define MOE_BLOCK_H
@@ -65,8 +66,9 @@ typedef struct moe_norm_dims {
  * At least one of y and yq.  The sum, the statistics and y are float32; the
  * norm reads s before its rounding.  Row sums of squares past float32's range
  * (elements above about 1e19) give rows of zeros, as float32 arithmetic does.
- * A row of zeros has yq = 0 and ys = 0.  A row whose y holds a NaN or an
- * infinity has yq = 0 and ys = NaN, so whatever is computed from it is NaN.
+ * A row of zeros has y = 0, yq = 0 and ys = 0 (with eps = 0 it has no norm: y
+ * is NaN).  A row whose y holds a NaN or an infinity has yq = 0 and ys = NaN,
+ * so whatever is computed from it is NaN.
  */
 int moe_add_rmsnorm(const moe_norm_dims *d, const void *x, const void *res, const float *weight,
                     void *sum, void *y, int8_t *yq, float *ys, void *stream);

@@ -138,6 +138,52 @@ def test_norm_in_place():
         assert torch.equal(r, s) and torch.equal(x, y)
 
 
+def test_norm_of_more_rows_than_one_grid_row_holds():
+    """Four rows a workgroup and 2^20 workgroups along x: the rows past 2^22 come along y."""
+    T, H = (1 << 22) + 9, 8
+    x = torch.arange(T * H, device="cuda", dtype=torch.float32).remainder_(97.0).sub_(48.5).to(torch.bfloat16).reshape(T, H)
+    w = torch.ones(H, device="cuda")
+    y, q, qs = torch.empty_like(x), torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_add_rmsnorm(moe.NormDims(T, H, moe.ELEM_BF16, 1e-6), x, None, w, None, y, q, qs)
+    for rows in (slice(0, 4096), slice(T - 4096, T)):
+        xv = f64(x[rows])
+        want = ref.norm(xv, None, np.ones(H), np.float32(1e-6))[1]
+        within(f64(y[rows]), want, (2.0 ** -8 + 64 * E32) * np.abs(want) * (1 + 1e-6), "y")
+        within(f64(q[rows]) * f64(qs[rows])[:, None], want, 0.501 * np.abs(want).max(axis=1, keepdims=True) / 127 + 0 * want,
+               "values")
+    dx, dw = torch.empty_like(x), torch.empty(H, device="cuda")
+    d = moe.NormDims(T, H, moe.ELEM_BF16, 1e-6)
+    n = moe.moe_add_rmsnorm_backward_ws_bytes(d)
+    moe.moe_add_rmsnorm_backward(d, x, w, y, None, dx, dw, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    xd, yd = x.double(), y.double()
+    rho = torch.rsqrt((xd * xd).mean(1, keepdim=True) + np.float64(np.float32(1e-6)))
+    terms = yd * xd * rho
+    # a lane adds T / (8 * 256) rows one after the other, then the folds and the partial sums
+    bound = (64 + T / 2048 + 1 + 3 + 80) * E32 * terms.abs().sum(0)
+    assert bool(((dw.double() - terms.sum(0)).abs() <= bound).all())
+
+
+def test_empty_batches():
+    """No rows: every entry point accepts empty tensors and writes nothing."""
+    e = dict(device="cuda")
+    x, q, s = torch.empty((0, 64), **e), torch.empty((0, 64), dtype=torch.int8, **e), torch.empty(0, **e)
+    w, dw = torch.ones(64, **e), torch.full((64,), 5.0, **e)
+    d, nd = moe.make_dims(0, 64, 64, 4, 2, 1), moe.NormDims(0, 64, moe.ELEM_F32, 1e-6)
+    tab = Tables(ref.routing(np.random.default_rng(0), 1, 4, 2, 128, 16, 1), 1)
+    moe.moe_add_rmsnorm(nd, x, x, w, x, x.clone(), q, s)
+    moe.moe_q8_quantize(nd, x, q, s)
+    moe.moe_q8_matmul(moe.Q8Dims(0, 64, 64, 0), q, s, torch.zeros((64, 64), dtype=torch.int8, **e), w, x)
+    moe.moe_q8_gate_up(d, q, s, tab.c, moe.Q8Bank(), None, x)
+    moe.moe_q8_down(d, tab.c, moe.Q8Bank(), None, q, s, x)
+    moe.moe_dispatch_rows(d, 0, x, tab.c, x)
+    moe.moe_combine_rows(d, 0, x, tab.c, x)
+    moe.moe_dispatch_rows_backward(d, 0, x, tab.c, x)
+    moe.moe_combine_rows_backward(d, 0, x, x, tab.c, x, s)
+    moe.moe_add_rmsnorm_backward(nd, x, w, x, None, x, dw, None, 0)
+    torch.cuda.synchronize()
+    assert bool((dw == 0).all()) and int(tab.status.item()) == 0
+
+
 def test_norm_rows_of_zeros_infinities_and_nans():
     """A row of zeros, one of the smallest values, one with an infinity, one with a NaN: each row's
     8-bit form stands on its own, and the others are as without them."""
@@ -159,7 +205,9 @@ def test_norm_rows_of_zeros_infinities_and_nans():
         torch.cuda.synchronize()
         for row in (0, 5):
             assert torch.equal(y[row], yc[row]) and torch.equal(q[row], qc[row]) and qs[row] == qsc[row]
-        if eps:
+        if not eps:
+            assert bool(torch.isnan(y[1]).all()) and torch.isnan(qs[1]) and bool((q[1] == 0).all())
+        else:
             assert bool((y[1] == 0).all()) and qs[1] == 0 and bool((q[1] == 0).all())
         for row in (3, 4):
             assert torch.isnan(qs[row]) and bool((q[row] == 0).all())

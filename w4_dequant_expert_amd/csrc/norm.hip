@@ -480,13 +480,12 @@ extern "C" {
 int moe_add_rmsnorm(const moe_norm_dims* d, const void* x, const void* res, const float* weight,
                     void* sum, void* y, int8_t* yq, float* ys, void* stream) {
   int rc = validate_norm(d);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!x || !weight || (!y && !yq) || (yq == nullptr) != (ys == nullptr) || (y && y == sum))
     return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(res, 16) || !aligned(weight, 16) || !aligned(sum, 16) ||
       !aligned(y, 16) || !aligned(yq, 16) || !aligned(ys, 4))
     return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   (void)hipGetLastError();
   return launched(launch_norm_any<true>(*d, x, res, weight, sum, y, yq, ys,
@@ -495,10 +494,9 @@ int moe_add_rmsnorm(const moe_norm_dims* d, const void* x, const void* res, cons
 
 int moe_q8_quantize(const moe_norm_dims* d, const void* x, int8_t* xq, float* xs, void* stream) {
   int rc = validate_norm(d);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!x || !xq || !xs) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(xs, 4)) return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   (void)hipGetLastError();
   return launched(launch_norm_any<false>(*d, x, nullptr, nullptr, nullptr, nullptr, xq, xs,
@@ -516,7 +514,7 @@ int moe_add_rmsnorm_backward(const moe_norm_dims* d, const void* sum, const floa
   int rc = validate_norm(d);
   if (rc) return rc;
   const size_t need = moe_add_rmsnorm_backward_ws_bytes(d);
-  if (!sum || !weight || !dy || !dx || (dweight && need && !ws)) return MOE_EINVAL;
+  if (d->T > 0 && (!sum || !weight || !dy || !dx || (dweight && !ws))) return MOE_EINVAL;
   if (!aligned(sum, 16) || !aligned(weight, 16) || !aligned(dy, 16) || !aligned(dsum, 16) ||
       !aligned(dx, 16) || !aligned(dweight, 4) || !aligned(ws, 16))
     return MOE_EALIGN;

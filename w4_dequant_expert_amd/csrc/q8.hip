@@ -656,11 +656,9 @@ hipError_t launch_grouped(const moe_dims& d, const Q8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int validate_grouped(const moe_dims* d, const moe_route_out* r, const void* xq, const void* xs,
-                     const void* out) {
-  int rc = validate_dims(d);
+int validate_grouped(const moe_route_out* r, const void* xq, const void* xs, const void* out) {
+  int rc = validate_route_out(r, false);
   if (rc) return rc;
-  if ((rc = validate_route_out(r, false))) return rc;
   if (!xq || !xs || !out) return MOE_EINVAL;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(out, 16)) return MOE_EALIGN;
   return MOE_OK;
@@ -705,10 +703,10 @@ int moe_q8_matmul(const moe_q8_dims* d, const int8_t* xq, const float* xs, const
   if (!d || d->M < 0 || d->M > (1 << 24) || d->N <= 0 || d->N % 8 || d->N > (1 << 20) || d->K <= 0 ||
       d->K % 64 || d->K > (1 << 16) || !elem_ok(d->type))
     return MOE_EINVAL;
+  if (d->M == 0) return MOE_OK;
   if (!xq || !xs || !wq || !ws || !out) return MOE_EINVAL;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(wq, 16) || !aligned(ws, 16) || !aligned(out, 16))
     return MOE_EALIGN;
-  if (d->M == 0) return MOE_OK;
   int rc = check_device();
   if (rc) return rc;
   Q8Args a{};
@@ -728,12 +726,12 @@ int moe_q8_matmul(const moe_q8_dims* d, const int8_t* xq, const float* xs, const
 
 int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const moe_route_out* r,
                    const moe_q8_bank* routed, const moe_q8_bank* shared, uint16_t* h, void* stream) {
-  int rc = validate_grouped(d, r, xq, xs, h);
-  if (rc) return rc;
+  int rc = validate_dims(d);
+  if (rc || d->T == 0) return rc;
+  if ((rc = validate_grouped(r, xq, xs, h))) return rc;
   if (!routed || (d->n_shared && !shared)) return MOE_EINVAL;
   if ((rc = validate_half(routed->gu, routed->gu_s))) return rc;
   if (d->n_shared && (rc = validate_half(shared->gu, shared->gu_s))) return rc;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   Q8Args a = grouped_args(*d, r, xq, xs, h, d->I);
   a.w = routed->gu;
@@ -749,12 +747,12 @@ int moe_q8_gate_up(const moe_dims* d, const int8_t* xq, const float* xs, const m
 int moe_q8_down(const moe_dims* d, const moe_route_out* r, const moe_q8_bank* routed,
                 const moe_q8_bank* shared, const int8_t* hq, const float* hs, uint16_t* y_slots,
                 void* stream) {
-  int rc = validate_grouped(d, r, hq, hs, y_slots);
-  if (rc) return rc;
+  int rc = validate_dims(d);
+  if (rc || d->T == 0) return rc;
+  if ((rc = validate_grouped(r, hq, hs, y_slots))) return rc;
   if (!routed || (d->n_shared && !shared)) return MOE_EINVAL;
   if ((rc = validate_half(routed->dn, routed->dn_s))) return rc;
   if (d->n_shared && (rc = validate_half(shared->dn, shared->dn_s))) return rc;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   Q8Args a = grouped_args(*d, r, hq, hs, y_slots, d->H);
   a.w = routed->dn;

@@ -171,7 +171,9 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_backward_kernel(
 int validate_rows(const moe_dims* d, int32_t type, const moe_route_out* r, bool weighted) {
   int rc = validate_dims(d);
   if (rc) return rc;
-  if (!elem_ok(type) || !r || !r->slot_pos || !r->status || (weighted && !r->topk_w)) return MOE_EINVAL;
+  if (!elem_ok(type)) return MOE_EINVAL;
+  if (d->T == 0) return MOE_OK;
+  if (!r || !r->slot_pos || !r->status || (weighted && !r->topk_w)) return MOE_EINVAL;
   if (!aligned(r->slot_pos, 4) || !aligned(r->status, 4) || (weighted && !aligned(r->topk_w, 4)))
     return MOE_EALIGN;
   return MOE_OK;
@@ -216,10 +218,9 @@ extern "C" {
 int moe_dispatch_rows(const moe_dims* d, int32_t type, const void* x, const moe_route_out* r,
                       void* rows, void* stream) {
   int rc = validate_rows(d, type, r, false);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!x || !rows) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(rows, 16)) return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   const int chunks = row_chunks(*d, type);
   const dim3 grid(static_cast<unsigned>(d->T), static_cast<unsigned>((chunks + kRowThreads - 1) / kRowThreads));
@@ -234,10 +235,9 @@ int moe_dispatch_rows(const moe_dims* d, int32_t type, const void* x, const moe_
 int moe_dispatch_rows_backward(const moe_dims* d, int32_t type, const void* drows,
                                const moe_route_out* r, void* dx, void* stream) {
   int rc = validate_rows(d, type, r, false);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!drows || !dx) return MOE_EINVAL;
   if (!aligned(drows, 16) || !aligned(dx, 16)) return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   return combine_any<false>(*d, type, drows, r, dx, stream);
 }
@@ -245,10 +245,9 @@ int moe_dispatch_rows_backward(const moe_dims* d, int32_t type, const void* drow
 int moe_combine_rows(const moe_dims* d, int32_t type, const void* rows, const moe_route_out* r,
                      void* y, void* stream) {
   int rc = validate_rows(d, type, r, true);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!rows || !y) return MOE_EINVAL;
   if (!aligned(rows, 16) || !aligned(y, 16)) return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   return combine_any<true>(*d, type, rows, r, y, stream);
 }
@@ -256,11 +255,10 @@ int moe_combine_rows(const moe_dims* d, int32_t type, const void* rows, const mo
 int moe_combine_rows_backward(const moe_dims* d, int32_t type, const void* dy, const void* rows,
                               const moe_route_out* r, void* drows, float* dtopk_w, void* stream) {
   int rc = validate_rows(d, type, r, true);
-  if (rc) return rc;
+  if (rc || d->T == 0) return rc;
   if (!dy || !drows || (dtopk_w && !rows)) return MOE_EINVAL;
   if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(drows, 16) || !aligned(dtopk_w, 4))
     return MOE_EALIGN;
-  if (d->T == 0) return MOE_OK;
   if ((rc = check_device())) return rc;
   const int chunks = row_chunks(*d, type);
   const dim3 grid(static_cast<unsigned>(d->T));
