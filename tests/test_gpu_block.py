@@ -76,7 +76,7 @@ def tiny(typ):
 # ----------------------------------------------------------------------------------- the norm
 
 # one wave, four and sixteen waves a row; rows that do not fill the last lane; one element group
-NORM_SIZES = [(1, 8), (3, 64), (1, 2048), (5, 2040), (2049, 520), (2050, 2048), (7, 2056), (3, 4096),
+NORM_SIZES = [(1, 8), (3, 64), (8, 2048), (9, 2048), (1, 2048), (5, 2040), (2049, 520), (2050, 2048), (7, 2056), (3, 4096),
               (2, 8192), (2, 8200), (3, 16384), (333, 1032)]
 
 
@@ -266,6 +266,11 @@ def test_norm_backward(T, H, typ):
         within(f64(dx), want, u * np.abs(want) * (1 + 1e-6) + 160 * E32 * size + tiny(typ), "dx")
         # rows of one lane (at most T / 512 + 1), 3 folds or none, partial sums (at most 64 + 16)
         within(f64(dw), wantw, (64 + T / 512 + 1 + 3 + 80) * E32 * sizew, "dweight")
+    # a dweight off the 16-byte grid (one workgroup writes an aligned one itself): the same bits
+    off = torch.empty(H + 1, device="cuda")[1:]
+    moe.moe_add_rmsnorm_backward(d, s, w, dy, None, dx, off, ws, n)
+    torch.cuda.synchronize()
+    assert torch.equal(off, dw)
     # without dweight: the same dx; over dy and over dsum: the same dx
     first, firstw = dx.clone(), dw.clone()
     dx.zero_()

@@ -437,13 +437,17 @@ hipError_t launch_norm_any(const moe_norm_dims& d, const void* x, const void* re
   return hipGetLastError();
 }
 
+// Waves per row of the gradient kernel: eight rows or fewer also go one wave
+// each, in one workgroup, whose sums are then dw already.
+int bwd_waves(int T, int H) { return H <= 2048 && T <= kBwdWaves ? 1 : row_waves(T, H); }
+
 // Workgroups of the gradient kernel: one per CU of eight waves, two of four
 // waves once there are rows for both, one of sixteen.  More of them hide more
 // latency but leave more partial sums to add.  Measured, us: 16384 x 2048 256
 // groups 50.7, 512 53; 333 x 2048 256 8.3, 512 9.5; 2000 x 2048 256 16.2, 512
 // 12.8, 1024 14.4; 2048 x 16384 128 69, 256 56, 512 64.
 int bwd_groups(const moe_norm_dims& d) {
-  const int nw = row_waves(d.T, d.H);
+  const int nw = bwd_waves(d.T, d.H);
   const int rows = nw == 1 ? kBwdWaves : 1;
   const int cap = nw == 4 && d.T >= 1024 ? 512 : 256;
   const int need = (d.T + rows - 1) / rows;
@@ -453,7 +457,7 @@ int bwd_groups(const moe_norm_dims& d) {
 template <int TYPE>
 void launch_bwd_type(const moe_norm_dims& d, const void* sum, const float* weight, const void* dy,
                      const void* dsum, void* dx, float* part, hipStream_t s) {
-  const int nw = row_waves(d.T, d.H);
+  const int nw = bwd_waves(d.T, d.H);
   const int c = (d.H / 8 + 64 * nw - 1) / (64 * nw);
   const dim3 grid(static_cast<unsigned>(bwd_groups(d)));
 #define MOE_BWD(NW, C)                                                                           \
@@ -522,7 +526,9 @@ int moe_add_rmsnorm_backward(const moe_norm_dims* d, const void* sum, const floa
   if (d->T == 0 && !dweight) return MOE_OK;
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* part = dweight ? static_cast<float*>(ws) : nullptr;
+  // one workgroup's partial sums are the sums (written in 16-byte pieces)
+  const bool direct = dweight && bwd_groups(*d) == 1 && aligned(dweight, 16);
+  float* part = direct ? dweight : dweight ? static_cast<float*>(ws) : nullptr;
   (void)hipGetLastError();
   if (d->T > 0) {
     switch (d->type) {
@@ -532,7 +538,7 @@ int moe_add_rmsnorm_backward(const moe_norm_dims* d, const void* sum, const floa
     }
     if ((rc = launched(hipGetLastError()))) return rc;
   }
-  if (dweight) {
+  if (dweight && !direct) {
     hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((d->H + 63) / 64)), dim3(1024), 0,
                        s, bwd_groups(*d), d->H, part, dweight);
     if ((rc = launched(hipGetLastError()))) return rc;
