@@ -337,7 +337,8 @@ def codes(rng, shape):
 
 PRODUCT_SIZES = [(1, 8, 64), (1, 8192, 2048), (2, 40, 64), (15, 136, 192), (16, 2048, 128), (17, 72, 320),
                  (32, 1000, 256), (33, 200, 64), (65, 264, 192), (127, 520, 576), (128, 128, 128),
-                 (200, 2056, 512), (333, 8192, 320), (513, 1032, 192), (2000, 8200, 128), (4097, 4104, 64)]
+                 (200, 2056, 512), (333, 8192, 320), (513, 1032, 192), (2000, 8200, 128), (4097, 4104, 64),
+                 (4000, 4360, 320), (4000, 4360, 512), (3900, 4360, 704)]
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
@@ -427,6 +428,8 @@ EXPERT_SIZES = [(1, 64, 64, 4, 1, 0, 16, 16), (1, 2048, 512, 256, 8, 1, 32, 16),
 EXPERT_SIZES += [(17, 128, 64, 64, 1, 1, 64, 16), (40, 192, 64, 64, 1, 1, 64, 16), (300, 128, 128, 300, 2, 1, 256, 16),
                  (1294, 192, 320, 105, 1, 1, 128, 16), (4096, 64, 512, 512, 1, 1, 256, 16),
                  (8192, 64, 1024, 1024, 1, 1, 256, 32)]
+# hundreds of rows an expert over several steps of inputs, an odd number of halves among them
+EXPERT_SIZES += [(1300, 448, 320, 4, 2, 1, 256, 16), (1100, 704, 512, 3, 1, 0, 256, 32)]
 
 
 def bank(rng, n, rows, K):

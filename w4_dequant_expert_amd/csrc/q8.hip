@@ -10,9 +10,13 @@
 // so a lane ends with runs of four neighbouring output channels of one row):
 //   q8_stream_kernel: few rows.  Bound by reading the weights once; every wave
 //     streams its share of K straight from memory into the matrix operands,
-//     with no LDS and no barrier until the waves' sums are added.
-//   q8_tile_kernel: many rows.  Bound by the int8 matrix rate; tiles of both
-//     operands go through LDS in steps of 128 inputs.
+//     with no LDS and no barrier until the waves' sums are added.  One row of
+//     2048 times 8192 columns: 4.9 us, 3.4 TB/s.
+//   q8_tile_kernel: more rows.  Tiles of both operands go through LDS in steps
+//     of 128 inputs.  Bound by the weights' bytes up to some hundred rows a
+//     matrix (512 tokens over 256 experts: 5.1 to 5.3 TB/s), then by what the
+//     L2s feed the copies: without its copies a step of the largest tile takes
+//     1.1 us, the time of its products, with them 1.5.
 #include <algorithm>
 
 #include "block.h"
@@ -259,7 +263,7 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // before.  The one barrier of a step stands before the products of its last
 // quarter, whose operands are in registers by then: behind it the next step is
 // in LDS and nobody reads this step's buffer any more, so the copies of step
-// s + R start into it at once and have R - 1 steps to land.
+// s + R start into it and have R - 1 steps to land.
 //
 // A staged row is 128 bytes, its 16-byte pieces XORed by the row (piece c of
 // row r at c ^ (r mod 8)), so that neighbouring rows of a fragment cover
@@ -291,7 +295,8 @@ __device__ __forceinline__ void copies_barrier() {
 // What a wave of a tile keeps over the steps.
 template <int WCOPY, int XCOPY>
 struct TileWave {
-  const int8_t* wp[WCOPY];  // this lane's weight row in each of the wave's copies
+  const int8_t* wbase[WCOPY];  // first weight row of each of the wave's copies (uniform)
+  uint32_t woff[WCOPY];        // this lane's bytes from there
   const int8_t* xp[XCOPY];  // and its token row
   int piece;                // the bytes of a step this lane copies
   int wave, wm, wn, lane;
@@ -369,23 +374,26 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-  auto copy = [&](int s, uint8_t* buf) {
-    // the last step may hold 64 inputs: its second half repeats the first
-    // (read into LDS, never multiplied)
+  // Copy i (0 .. COPIES-1) of step s: the wave's weight rows, then its token
+  // rows.  The last step may hold 64 inputs: its second half repeats the first
+  // (read into LDS, never multiplied).
+  auto copy_one = [&](int s, uint8_t* buf, int i) {
     const int at = s * kStep + t.piece;
     const int k0 = at < a.K ? at : at - 64;
-    if (GROUPED && WM * M <= 2 && blk.once) {
-#pragma unroll
-      for (int i = 0; i < WCOPY; ++i)
-        __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, kNonTemporal);
+    if (i < WCOPY) {
+      uint8_t* const to = buf + (i * WAVES + t.wave) * 1024;
+      if (GROUPED && WM * M <= 2 && blk.once)
+        __builtin_amdgcn_global_load_lds(t.wbase[i] + (t.woff[i] + static_cast<uint32_t>(k0)), to, 16, 0, kNonTemporal);
+      else
+        __builtin_amdgcn_global_load_lds(t.wbase[i] + (t.woff[i] + static_cast<uint32_t>(k0)), to, 16, 0, 0);
     } else {
-#pragma unroll
-      for (int i = 0; i < WCOPY; ++i)
-        __builtin_amdgcn_global_load_lds(t.wp[i] + k0, buf + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(t.xp[i - WCOPY] + k0, buf + BN * kStep + ((i - WCOPY) * WAVES + t.wave) * 1024,
+                                       16, 0, 0);
     }
+  };
+  auto copy = [&](int s, uint8_t* buf) {
 #pragma unroll
-    for (int i = 0; i < XC; ++i)
-      __builtin_amdgcn_global_load_lds(t.xp[i] + k0, buf + BN * kStep + (i * WAVES + t.wave) * 1024, 16, 0, 0);
+    for (int i = 0; i < COPIES; ++i) copy_one(s, buf, i);
   };
   struct Frags {
     uint4 w[NT], x[M];
@@ -409,33 +417,57 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
         if (i * NT + j >= lo && i * NT + j < hi) acc[i][j] = mfma32(f.w[j], f.x[i], acc[i][j]);
   };
   Frags fa, fb;
+  // Products lo .. of f with copies c0 .. c1-1 of step s started between them.
+  auto spread = [&](const Frags& f, int lo, bool on, int s, uint8_t* buf, int c0, int c1) {
+    const int n = c1 - c0, left = M * NT - lo;
+#pragma unroll
+    for (int c = 0; c < n; ++c) {
+      if (on) copy_one(s, buf, c0 + c);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(f, lo + left * c / n, lo + left * (c + 1) / n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (n == 0) multiply(f, lo, M * NT);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   // One quarter: its products from f, quarter q of buf read into g behind the
   // first of them (so that the wait for f stands ahead of the newer reads).
-  auto quarter = [&](const Frags& f, Frags& g, const uint8_t* buf, int q) {
+  auto quarter = [&](const Frags& f, Frags& g, const uint8_t* buf, int q, bool on, int s, uint8_t* to, int c0, int c1) {
     multiply(f, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
     read(g, buf, q);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(f, 1, M * NT);
-    __builtin_amdgcn_sched_barrier(0);
+    spread(f, 1, on, s, to, c0, c1);
   };
+  // With eight waves a step's copies keep the address path busy for about half
+  // of the step's products, and a wave that waits there multiplies nothing: two
+  // eighths of them are started in the quarter behind the barrier, three in the
+  // next step's first quarter and three in its second, between the products
+  // (16384x8192x4096: 509 us in one run behind the barrier, 475 spread).
+  constexpr bool SPREAD = WAVES >= 8;
+  constexpr int C1 = SPREAD ? (COPIES * 2 + 7) / 8 : COPIES, C2 = SPREAD ? (COPIES * 5 + 7) / 8 : COPIES;
   // Step s from its first quarter's operands in fa; leaves the next step's
-  // there.  full: the R - 1 steps after it are there.
-  auto step = [&](int s, bool full, uint8_t* cur, uint8_t* next) {
-    quarter(fa, fb, cur, 1);
+  // there.  full: the R - 1 steps after it are there.  prev: the buffer that
+  // step s - 1 freed, whose copies (of step s + R - 1) go on under this step.
+  auto step = [&](int s, bool full, uint8_t* cur, uint8_t* next, uint8_t* prev) {
+    const bool on = SPREAD && s > 0 && s + R - 1 < nk;
+    quarter(fa, fb, cur, 1, on, s + R - 1, prev, C1, C2);
     if ((s + 1) * kStep <= a.K) {  // else 64 inputs: two quarters
-      quarter(fb, fa, cur, 2);
-      quarter(fa, fb, cur, 3);
+      quarter(fb, fa, cur, 2, on, s + R - 1, prev, C2, COPIES);
+      quarter(fa, fb, cur, 3, false, 0, prev, 0, 0);
     }
     if (full || s + R - 1 < nk)
       copies_barrier<(R - 2) * COPIES>();
     else
       copies_barrier<0>();
-    if (s + R < nk) copy(s + R, cur);
     __builtin_amdgcn_sched_barrier(0);
+    if (!SPREAD && s + R < nk) copy(s + R, cur);
     if (full || s + 1 < nk) read(fa, next, 0);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(fb, 0, M * NT);
+    if (SPREAD)
+      spread(fb, 0, s + R < nk, s + R, cur, 0, C1);
+    else
+      multiply(fb, 0, M * NT);
     __builtin_amdgcn_sched_barrier(0);
   };
   uint8_t* const ring[4] = {b0, b1, b2, b3};
@@ -450,11 +482,11 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
   int s = 0;
   for (; s + 2 * R - 2 < nk; s += R)
 #pragma unroll
-    for (int i = 0; i < R; ++i) step(s + i, true, ring[i], ring[(i + 1) % R]);
+    for (int i = 0; i < R; ++i) step(s + i, true, ring[i], ring[(i + 1) % R], ring[(i + R - 1) % R]);
   for (; s < nk; s += R)
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (s + i < nk) step(s + i, false, ring[i], ring[(i + 1) % R]);
+      if (s + i < nk) step(s + i, false, ring[i], ring[(i + 1) % R], ring[(i + R - 1) % R]);
   // Every wave has read its last operands (the last step's barrier): its share
   // of the buffers holds its outputs, 32 rows at a time, on the way to
   // whole-line stores.
@@ -557,10 +589,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
   const int crow = lane >> 3;
   t.piece = ((lane & 7) ^ crow) * 16;
 #pragma unroll
-  for (int i = 0; i < WCOPY; ++i)
-    t.wp[i] = blk.w +
-              static_cast<size_t>(q8_weight_row<SWIGLU, 32>(v0 + (i * WAVES + wave) * 8 + crow, a.N)) * a.K;
-  for (int m0 = 0; m0 < blk.rows; m0 += BM) {
+  for (int i = 0; i < WCOPY; ++i) {
+    // the eight rows of a copy lie in one run of gate or up rows
+    const int v = v0 + (i * WAVES + wave) * 8;
+    const int first = uniform(q8_weight_row<SWIGLU, 32>(v, a.N));
+    t.wbase[i] = blk.w + static_cast<size_t>(first) * a.K;
+    t.woff[i] = static_cast<uint32_t>(q8_weight_row<SWIGLU, 32>(v + crow, a.N) - first) * a.K;
+  }
+  // moe_route cuts experts at 256 rows at most: the largest tile takes any block at once
+  if (BM >= 256 && blk.rows > BM) {
+    if (threadIdx.x == 0) status_set(a.status, MOE_STATUS_BAD_INDEX);
+    return;
+  }
+  for (int m0 = 0; m0 < (BM >= 256 ? 1 : blk.rows); m0 += BM) {
     const int mt = (min(BM, blk.rows - m0) + WM * 32 - 1) / (WM * 32);
 #pragma unroll
     for (int i = 0; i < XCOPY; ++i) {
@@ -590,8 +631,8 @@ void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
                      dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
 
-// Which kernel.  Every one of them takes any number of rows (those past its
-// tile in another pass over the weights), so the choice is speed alone.
+// Which kernel.  Every one of them takes any block (rows past its tile go in
+// another pass over the weights), so the choice is speed alone.
 //
 // Dense: few rows stream the weights, with narrower workgroups where there are
 // few columns (1 x 2048 x 2048: 16 columns a workgroup 3.3 us, 32 columns 4.1);
@@ -601,7 +642,7 @@ void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
 //   64 x 64, four buffers              8.5       8.4      18.1       40.0       20.7
 //   64 x 64, two buffers              11.1      10.3      14.2       32.8       17.2
 //   128 x 128                         11.6      11.4      14.9       23.0       15.9
-// and 16384x8192: 256 x 256 333, 128 x 128 447.
+// and 16384x8192: 256 x 256 282 (1.95 PFLOP/s; 2.44 at 8192 cubed), 128 x 128 345.
 hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
   const auto tiles = [&](int bm, int bn) { return static_cast<long long>(cdiv(a.rows, bm)) * cdiv(a.N, bn); };
   if (a.rows <= 16) {
@@ -637,8 +678,8 @@ hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
 //   128 x 128       91       98     123      106       122       145       159       216       502
 //   256 x 256      103      107     134      114       134       153       155       186       437
 // (128 tokens in blocks of at most 32: stream 82, 32 x 128 84; 512 in blocks of
-// at most 16: stream 146, 32 x 128 123.)  Weights that are
-// read once are copied past the caches (512 tokens, down: 60 us -> 57).
+// at most 16: stream 146, 32 x 128 123.)  Weights that are read once are copied
+// past the caches (512 tokens, down: 60 us -> 57).
 template <bool GATHER, bool SWIGLU>
 hipError_t launch_grouped(const moe_dims& d, const Q8Args& a, hipStream_t s) {
   const int mean = cdiv(d.T * d.k, d.E);
