@@ -266,9 +266,9 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // s + R start into it and have R - 1 steps to land.
 //
 // A staged row is 128 bytes, its 16-byte pieces XORed by the row (piece c of
-// row r at c ^ (r mod 8)), so that neighbouring rows of a fragment cover
-// different banks.  A copy moves eight rows, lane l's 16 bytes landing at byte
-// 16 l: the permutation is made by the address each lane reads.  Rows past the
+// row r at c ^ (r / 2 mod 8)), so that any sixteen neighbouring rows of a
+// fragment cover all 64 banks.  A copy moves eight rows, lane l's 16 bytes
+// landing at byte 16 l: the permutation is made by the address each lane reads.  Rows past the
 // block repeat its last row and columns past N the last column; they only
 // reach outputs that are not stored.
 //
@@ -315,6 +315,8 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
   constexpr int ELEM = TYPE == MOE_ELEM_F32 ? 4 : 2;
   constexpr int COLS = (SWIGLU ? NT / 2 : NT) * 32, PIECES = COLS * ELEM / 16;
   const int r32 = lane & 31, hi = lane >> 5;
+  // XOR of a row's pieces: sixteen rows' pieces cover all banks (256 bytes)
+  const auto turn = [](int r) { return (r * PIECES / 16) & (PIECES - 1); };
 #pragma unroll
   for (int j = 0; j < NT; j += SWIGLU ? 2 : 1) {
     const int cj = SWIGLU ? j / 2 * 32 : j * 32;
@@ -331,7 +333,7 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
         q8_scale(xs, sc[j][g], s0, o);
       }
       const int byte = c * ELEM;
-      uint8_t* const to = out + r32 * PIECES * 16 + (((byte >> 4) ^ (r32 & (PIECES - 1))) << 4);
+      uint8_t* const to = out + r32 * PIECES * 16 + (((byte >> 4) ^ turn(r32)) << 4);
       store4(to + (byte & 15), 0, TYPE, o);
     }
   }
@@ -340,7 +342,7 @@ __device__ __forceinline__ void q8_tile_out(const Q8Args& a, const Q8Block& blk,
 #pragma unroll
   for (int it = 0; it < 32 * PIECES / 64; ++it) {
     const int r = (it * 64 + lane) / PIECES, piece = (it * 64 + lane) % PIECES;
-    const uint4 v = *reinterpret_cast<const uint4*>(out + r * PIECES * 16 + ((piece ^ (r & (PIECES - 1))) << 4));
+    const uint4 v = *reinterpret_cast<const uint4*>(out + r * PIECES * 16 + ((piece ^ turn(r)) << 4));
     const int c = c0 + piece * (16 / ELEM);
     if (m1 + r < blk.rows && c < n_out && ((stored >> r) & 1)) {
       uint4* const to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
@@ -400,7 +402,7 @@ __device__ __forceinline__ void q8_tile_rows(const Q8Args& a, const Q8Block& blk
   };
   // quarter q (inputs 32q .. 32q+31) of a step
   auto read = [&](Frags& f, const uint8_t* buf, int q) {
-    const int at = r32 * kStep + (((2 * q + hi) ^ (r32 & 7)) << 4);
+    const int at = r32 * kStep + (((2 * q + hi) ^ ((r32 >> 1) & 7)) << 4);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       f.w[j] = *reinterpret_cast<const uint4*>(buf + (t.wn * NT + j) * 32 * kStep + at);
@@ -587,7 +589,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
   t.wm = wave / WN;
   t.wn = wave % WN;
   const int crow = lane >> 3;
-  t.piece = ((lane & 7) ^ crow) * 16;
+  // copy i of a wave starts at row 8 (i WAVES + wave): r / 2 mod 8 is known up to its wave's parity
+  static_assert(WAVES % 2 == 0, "copies of a wave share their parity");
+  t.piece = ((lane & 7) ^ ((crow >> 1) + 4 * (wave & 1))) * 16;
 #pragma unroll
   for (int i = 0; i < WCOPY; ++i) {
     // the eight rows of a copy lie in one run of gate or up rows
