@@ -701,6 +701,20 @@ def test_layer_in_8_bits(T):
     torch.cuda.synchronize()
     err = np.linalg.norm(f64(y2) - want, axis=1) / np.linalg.norm(want, axis=1)
     assert err.max() <= 4 * 2.0 ** -8 + 2.0 / 127 * 4, err.max()
+    # the stages on their own: the same bits
+    h, ys, xn = layer.h.clone(), layer.y_slots.clone(), layer.xn[:T].clone()
+    layer.h.zero_()
+    layer.xq.zero_()
+    d = layer.route(xn)
+    layer.gate_up(d, xn)
+    layer.down(d)
+    y3 = torch.empty_like(y)
+    layer.combine(d, y3)
+    torch.cuda.synchronize()
+    rows = T * (k + 1)
+    assert torch.equal(layer.h[:rows], h[:rows]) and torch.equal(layer.y_slots[:rows], ys[:rows]) and torch.equal(y3, y2)
+    with pytest.raises(NotImplementedError):
+        layer.shared_ffn(d, xn)
 
 
 def test_layer_in_4_bits_behind_the_norm():

@@ -268,9 +268,9 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // A staged row is 128 bytes, its 16-byte pieces XORed by the row (piece c of
 // row r at c ^ (r / 2 mod 8)), so that any sixteen neighbouring rows of a
 // fragment cover all 64 banks.  A copy moves eight rows, lane l's 16 bytes
-// landing at byte 16 l: the permutation is made by the address each lane reads.  Rows past the
-// block repeat its last row and columns past N the last column; they only
-// reach outputs that are not stored.
+// landing at byte 16 l: the permutation is made by the address each lane reads.
+// Rows past the block repeat its last row and columns past N the last column;
+// they only reach outputs that are not stored.
 //
 // Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8)
 // in contiguous runs, each run going through groups of four row blocks column
@@ -281,9 +281,9 @@ constexpr int kStep = 128;
 constexpr int kNonTemporal = 2;  // cache policy of a copy whose data nobody else reads
 
 // At most N of this wave's copies are still in flight, its LDS reads are done
-// and every wave is here.  The wait is the builtin, which the compiler's own bookkeeping of waits
-// takes into account; the empty statements keep LDS accesses from moving
-// across.
+// and every wave is here.  The wait is the builtin, which the compiler's own
+// bookkeeping of waits takes into account; the empty statements keep LDS
+// accesses from moving across.
 template <int N>
 __device__ __forceinline__ void copies_barrier() {
   asm volatile("" ::: "memory");
@@ -297,8 +297,8 @@ template <int WCOPY, int XCOPY>
 struct TileWave {
   const int8_t* wbase[WCOPY];  // first weight row of each of the wave's copies (uniform)
   uint32_t woff[WCOPY];        // this lane's bytes from there
-  const int8_t* xp[XCOPY];  // and its token row
-  int piece;                // the bytes of a step this lane copies
+  const int8_t* xp[XCOPY];     // its token row in each
+  int piece;                   // the bytes of a step this lane copies
   int wave, wm, wn, lane;
 };
 

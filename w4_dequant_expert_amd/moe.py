@@ -606,6 +606,7 @@ class MoeLayer:
         rows = T_max * k + (T_max if n_shared else 0)
         self.h = torch.empty((rows, I), dtype=torch.int16, device=device)
         self.y_slots = torch.empty((rows, H), dtype=torch.int16, device=device)
+        self.xn = torch.empty((T_max, H), dtype=torch.int16, device=device)  # forward_residual's normed rows
 
     def dims(self, T):
         if T > self.T_max:
@@ -661,16 +662,10 @@ class MoeLayer:
         self.ffn_combine(d, x, y, routed, shared, stream)
         return y
 
-    def _norm_buffers(self, device):
-        import torch
-        if getattr(self, "xn", None) is None:
-            self.xn = torch.empty((self.T_max, self.H), dtype=torch.int16, device=device)
-
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
         """The layer with what stands in front of it: res += x in place, then
         the layer on the RMS norm of the sum (bfloat16 rows, one norm call)."""
         d = self.dims(x.shape[0])
-        self._norm_buffers(x.device)
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         stream=stream)
         return self.forward(self.xn[:d.T], y, stream=stream)
@@ -678,8 +673,8 @@ class MoeLayer:
 
 class Q8MoeLayer(MoeLayer):
     """The same layer with 8-bit banks (DeviceBankQ8): routing and combine as in
-    MoeLayer, the products in 8-bit integers.  forward(x, y) quantises the
-    tokens itself; forward_residual gets them from the norm."""
+    MoeLayer, the products in 8-bit integers.  gate_up, and so forward, quantises
+    the tokens itself; forward_residual gets them from the norm."""
 
     def __init__(self, *args, device="cuda", **kw):
         import torch
@@ -691,7 +686,10 @@ class Q8MoeLayer(MoeLayer):
         self.hs = torch.empty((rows,), dtype=torch.float32, device=device)
 
     def gate_up(self, d, x, routed=None, shared=None, stream=None):
-        """h from the quantised tokens in xq and xs (x is not read)."""
+        moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
+        self._gate_up_quantised(d, routed, shared, stream)
+
+    def _gate_up_quantised(self, d, routed=None, shared=None, stream=None):
         r = routed or self.routed
         s = shared or self.shared
         moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, r.c, s.c if s is not None else None, self.h,
@@ -705,7 +703,6 @@ class Q8MoeLayer(MoeLayer):
                     stream)
 
     def ffn(self, d, x, routed=None, shared=None, stream=None):
-        moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
         self.gate_up(d, x, routed, shared, stream)
         self.down(d, routed, shared, stream)
 
@@ -720,12 +717,10 @@ class Q8MoeLayer(MoeLayer):
 
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
         d = self.dims(x.shape[0])
-        self._norm_buffers(x.device)
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         self.xq, self.xs, stream)
-        xn = self.xn[:d.T]
-        self.route(xn, stream=stream)
-        self.gate_up(d, xn, stream=stream)
+        self.route(self.xn[:d.T], stream=stream)
+        self._gate_up_quantised(d, stream=stream)
         self.down(d, stream=stream)
         self.combine(d, y, stream)
         return y
