@@ -685,8 +685,10 @@ hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
 //   128 x 128       91       98     123      106       122       145       159       216       502
 //   256 x 256      103      107     134      114       134       153       155       186       437
 // (128 tokens in blocks of at most 32: stream 82, 32 x 128 84; 512 in blocks of
-// at most 16: stream 146, 32 x 128 123.)  Weights that are read once are copied
-// past the caches (512 tokens, down: 60 us -> 57).
+// at most 16: stream 146, 32 x 128 123.  All rows were measured with one deal of
+// the tiles; dealt block by block, as now, the largest tile takes 144 at
+// 2048/256, 186 at 4096/128 and 411 at 16384/256.)  Weights that are read once
+// are copied past the caches (512 tokens, down: 60 us -> 57).
 template <bool GATHER, bool SWIGLU>
 hipError_t launch_grouped(const moe_dims& d, const Q8Args& a, hipStream_t s) {
   const int mean = cdiv(d.T * d.k, d.E);
