@@ -124,12 +124,16 @@ def _routing(g, T, E, k, tile, n_shared=1):
             lo, hi = c * b // nb, c * (b + 1) // nb
             blocks.append([e, row + lo, hi - lo, -(-(-(-c // nb)) // 16) * 16])
         row += c
+    n_blocks = len(blocks)
+    # the table holds moe_max_blocks entries, as the calls ask for; those behind the map stay empty
+    S, cut = T * k, -(-T // tile)
+    blocks += [[0, 0, 0, 0]] * (S // tile + min(S, E) + n_shared * cut - n_blocks)
     i32 = dict(dtype=torch.int32, device=DEV)
     offsets = torch.zeros(E + 1, **i32)
     offsets[1:] = counts.cumsum(0)
     return dict(topk_idx=idx.to(torch.int32), topk_w=w.contiguous(), counts=counts.to(torch.int32),
                 offsets=offsets, sorted_slot=order.to(torch.int32), slot_pos=pos.to(torch.int32),
-                blocks=torch.tensor(blocks, **i32).reshape(-1, 4), n_blocks=torch.tensor([len(blocks)], **i32),
+                blocks=torch.tensor(blocks, **i32).reshape(-1, 4), n_blocks=torch.tensor([n_blocks], **i32),
                 status=torch.zeros(1, **i32), cmax=int(counts.max()) if T else 0)
 
 
