@@ -57,11 +57,10 @@ struct Q8Block {
 };
 
 // Block b < max_blocks of the map; false past its end, and (with the status
-// bit) for an entry out of range.  The entry and the map's length are loaded
-// together.
+// bit) for an entry out of range.
 __device__ __forceinline__ bool q8_block(const Q8Args& a, int b, Q8Block& o) {
-  const int4 e = reinterpret_cast<const int4*>(a.blocks)[b];
-  if (b >= *a.n_blocks) return false;
+  int4 e;
+  if (!map_entry(reinterpret_cast<const int4*>(a.blocks), a.n_blocks, b, e)) return false;
   const int g = uniform(e.x);
   o.row0 = uniform(e.y);
   o.rows = uniform(e.z);
