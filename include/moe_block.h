@@ -150,8 +150,9 @@ typedef struct moe_q8_bank {
  *   r  tables from moe_route;  routed bank of E experts;  shared bank of 1
  *      expert, or NULL if n_shared = 0
  *   h  [Rows][I] bfloat16 (16-byte aligned)
- * Table entries out of range set MOE_STATUS_BAD_INDEX and are skipped.  Entries
- * of r->blocks behind the first *r->n_blocks are not read.
+ * Table entries out of range, blocks of more than d->tile_m_max rows among them,
+ * set MOE_STATUS_BAD_INDEX and are skipped.  Entries of r->blocks behind the
+ * first *r->n_blocks are not read.
  */
 int moe_q8_gate_up(const moe_dims *d, const int8_t *xq, const float *xs, const moe_route_out *r,
                    const moe_q8_bank *routed, const moe_q8_bank *shared, uint16_t *h, void *stream);

@@ -1,0 +1,56 @@
+"""Edges of the operators of include/moe_block.h on the GPU: table entries that
+only some kernels would take, launches and batches past a limit, the streamed
+forms, and the layer's checks.  References and bounds as in test_gpu_block.py."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import block_ref as ref  # noqa: E402
+import w4_dequant_expert_amd as moe  # noqa: E402
+from test_gpu_block import Tables, bank, codes, f32  # noqa: E402
+
+
+# tokens, experts, tile_m_max: one for each kernel of the grouped products
+@pytest.mark.parametrize("T,E,tile", [(8, 8, 16), (40, 6, 32), (100, 6, 64), (300, 4, 128), (600, 4, 256)])
+def test_a_block_taller_than_the_map_allows_is_refused_by_every_kernel(T, E, tile):
+    print(f"tall block {T} {E} {tile}", flush=True)
+    H, I, k = 128, 64, 2
+    rng = np.random.default_rng(T)
+    r = ref.routing(rng, T, E, k, tile, 16, 1)
+    d = moe.make_dims(T, H, I, E, k, 1, tile, 16)
+    rows = T * (k + 1)
+    gq, gs, _, _ = bank(rng, E + 1, 2 * I, H)
+    dq, ds, _, _ = bank(rng, E + 1, H, I)
+    xq, _ = codes(rng, (T, H))
+    xs, _ = f32(rng, T, 0.0005, 0.002)
+    hq, _ = codes(rng, (rows, I))
+    hs, _ = f32(rng, rows, 0.0005, 0.002)
+    routed = moe.Q8Bank(gq.data_ptr(), gs.data_ptr(), dq.data_ptr(), ds.data_ptr())
+    shared = moe.Q8Bank(gq[E].data_ptr(), gs[E].data_ptr(), dq[E].data_ptr(), ds[E].data_ptr())
+
+    def run(r):
+        tab = Tables(r, T)
+        h = torch.zeros((rows, I), dtype=torch.bfloat16, device="cuda")
+        y = torch.zeros((rows, H), dtype=torch.bfloat16, device="cuda")
+        moe.moe_q8_gate_up(d, xq, xs, tab.c, routed, shared, h)
+        up = int(tab.status.item())
+        tab.status.zero_()
+        moe.moe_q8_down(d, tab.c, routed, shared, hq, hs, y)
+        torch.cuda.synchronize()
+        return h, y, up, int(tab.status.item())
+
+    h, y, up, down = run(r)
+    assert up == 0 and down == 0
+    b = {n: v.copy() for n, v in r.items()}
+    lost = slice(0, int(b["blocks"][0, 2]))
+    b["blocks"][0, 2] = tile + 1
+    h2, y2, up, down = run(b)
+    assert up & moe.STATUS_BAD_INDEX and down & moe.STATUS_BAD_INDEX
+    for got, want in ((h2, h), (y2, y)):
+        assert bool((got[lost] == 0).all()) and torch.equal(got[lost.stop:], want[lost.stop:])

@@ -45,7 +45,7 @@ struct Q8Args {
   const int32_t* n_blocks;
   const int32_t* sorted_slot;
   uint32_t* status;
-  int max_blocks, E, T, k, n_shared;
+  int max_blocks, E, T, k, n_shared, tile_m_max;
 };
 
 // A block of output rows that share one weight matrix.
@@ -57,7 +57,8 @@ struct Q8Block {
 };
 
 // Block b < max_blocks of the map; false past its end, and (with the status
-// bit) for an entry out of range.
+// bit) for an entry out of range.  One of more than tile_m_max rows counts as
+// such for every kernel, so that which one is chosen never decides it.
 __device__ __forceinline__ bool q8_block(const Q8Args& a, int b, Q8Block& o) {
   int4 e;
   if (!map_entry(reinterpret_cast<const int4*>(a.blocks), a.n_blocks, b, e)) return false;
@@ -66,7 +67,7 @@ __device__ __forceinline__ bool q8_block(const Q8Args& a, int b, Q8Block& o) {
   o.rows = uniform(e.z);
   const bool shared = g == a.E;
   if (g < 0 || g > a.E || (shared && !a.n_shared) || o.row0 < 0 || o.rows <= 0 ||
-      o.rows > a.rows - o.row0) {
+      o.rows > min(a.tile_m_max, a.rows - o.row0)) {
     if (threadIdx.x == 0) status_set(a.status, MOE_STATUS_BAD_INDEX);
     return false;
   }
@@ -602,11 +603,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
     t.wbase[i] = blk.w + static_cast<size_t>(first) * a.K;
     t.woff[i] = static_cast<uint32_t>(q8_weight_row<SWIGLU, 32>(v + crow, a.N) - first) * a.K;
   }
-  // moe_route cuts experts at 256 rows at most: the largest tile takes any block at once
-  if (BM >= 256 && blk.rows > BM) {
-    if (threadIdx.x == 0) status_set(a.status, MOE_STATUS_BAD_INDEX);
-    return;
-  }
+  // blocks have tile_m_max rows at most, which is 256 at most: one pass of the largest tile
   for (int m0 = 0; m0 < (BM >= 256 ? 1 : blk.rows); m0 += BM) {
     const int mt = (min(BM, blk.rows - m0) + WM * 32 - 1) / (WM * 32);
 #pragma unroll
@@ -637,8 +634,8 @@ void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
                      dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
 
-// Which kernel.  Every one of them takes any block (rows past its tile go in
-// another pass over the weights), so the choice is speed alone.
+// Which kernel.  Every one of them takes any block of a map (rows past its tile
+// go in another pass over the weights), so the choice is speed alone.
 //
 // Dense: few rows stream the weights, with narrower workgroups where there are
 // few columns (1 x 2048 x 2048: 16 columns a workgroup 3.3 us, 32 columns 4.1);
@@ -737,6 +734,7 @@ Q8Args grouped_args(const moe_dims& d, const moe_route_out* r, const int8_t* xq,
   a.T = d.T;
   a.k = d.k;
   a.n_shared = d.n_shared;
+  a.tile_m_max = d.tile_m_max;
   return a;
 }
 
