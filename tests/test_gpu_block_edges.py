@@ -54,3 +54,36 @@ def test_a_block_taller_than_the_map_allows_is_refused_by_every_kernel(T, E, til
     assert up & moe.STATUS_BAD_INDEX and down & moe.STATUS_BAD_INDEX
     for got, want in ((h2, h), (y2, y)):
         assert bool((got[lost] == 0).all()) and torch.equal(got[lost.stop:], want[lost.stop:])
+
+
+def test_a_launch_of_more_than_2_32_threads():
+    """A million tokens in blocks of 16 rows: more workgroups than a launch holds along x.  The map here
+    ends after a few blocks, and the arrays hold those blocks' rows alone."""
+    T, H, I, E, k = 1 << 20, 8192, 64, 64, 8
+    d = moe.make_dims(T, H, I, E, k, 0, 16, 16)
+    S = T * k
+    assert moe.moe_max_blocks(d) * (H // 128) * 128 >= 2 ** 32
+    rng = np.random.default_rng(12)
+    n = 2000
+    at = np.arange(0, n, 16)
+    blocks = np.zeros((moe.moe_max_blocks(d), 4), np.int32)
+    blocks[:len(at)] = [[i % E, a, min(16, n - a), 16] for i, a in enumerate(at)]
+    tab = dict(topk_idx=np.zeros(1, np.int32), topk_w=np.zeros(1, np.float32), counts=np.zeros(E, np.int32),
+               offsets=np.zeros(E + 1, np.int32), sorted_slot=np.zeros(1, np.int32), slot_pos=np.zeros(1, np.int32),
+               blocks=blocks, n_blocks=np.array([len(at)], np.int32))
+    tab = Tables(tab, T)
+    q, s, qv, sv = bank(rng, E, H, I)
+    hq, hv = codes(rng, (n, I))
+    hs, hsv = f32(rng, n, 0.0005, 0.002)
+    y = torch.zeros((n, H), dtype=torch.bfloat16, device="cuda")
+    assert S > n   # the binding would ask for all rows: raw addresses
+    moe.moe_q8_down(d, tab.c, moe.Q8Bank(dn=q.data_ptr(), dn_s=s.data_ptr()), None, hq.data_ptr(), hs.data_ptr(),
+                    y.data_ptr())
+    torch.cuda.synchronize()
+    group = np.arange(n) // 16 % E
+    for g in np.unique(group):
+        m = group == g
+        want = ref.product(hv[m], hsv[m], qv[g], sv[g])
+        got = y[torch.from_numpy(m).cuda()].double().cpu().numpy()
+        assert (np.abs(got - want) <= (2.0 ** -8 + 3 * ref.EPS32) * np.abs(want) * (1 + 1e-6) + 1e-37).all()
+    assert int(tab.status.item()) == 0

@@ -27,6 +27,15 @@ __host__ __device__ inline bool map_entry(const int4* blocks, const int32_t* n, 
   return true;
 }
 
+// Launches of more workgroups than x takes (a launch holds fewer than 2^32
+// threads in x): rows of kGridX of them along y.  Workgroups of the last row
+// past the count find no work.
+constexpr unsigned kGridX = 1u << 20;
+inline dim3 grid_of(unsigned groups) {
+  return dim3(groups < kGridX ? groups : kGridX, (groups + kGridX - 1) / kGridX);
+}
+__device__ __forceinline__ unsigned workgroup() { return blockIdx.y * kGridX + blockIdx.x; }
+
 // ---------------------------------------------------------------------------
 // Row elements.  Elem<TYPE>::V elements make one 16-byte access.
 // ---------------------------------------------------------------------------

@@ -22,7 +22,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxNormH = 16384;
-constexpr unsigned kGridX = 1u << 20;  // workgroups along x: a launch holds fewer than 2^32 threads in x
 
 // Eight elements of a row, raw.
 template <int TYPE>
@@ -124,7 +123,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void add_rmsnorm_kernel(
   __shared__ float red_s[NW];
   __shared__ uint32_t red_m[NW];
   const int wave = uniform(threadIdx.x >> 6);
-  const int group = static_cast<int>(blockIdx.y * kGridX + blockIdx.x);
+  const int group = static_cast<int>(workgroup());
   const int row = NW == 1 ? group * 4 + wave : group;
   if (row >= T) return;  // whole waves (NW = 1) or whole workgroups
   const int li = NW == 1 ? (threadIdx.x & 63) : threadIdx.x;
@@ -404,7 +403,7 @@ void launch_norm(const moe_norm_dims& d, const void* x, const void* res, const f
   const unsigned groups = static_cast<unsigned>((d.T + rows - 1) / rows);
   hipLaunchKernelGGL((streamed(d) ? add_rmsnorm_kernel<TYPE, NW, C, NORM, true>
                                   : add_rmsnorm_kernel<TYPE, NW, C, NORM, false>),
-                     dim3(groups < kGridX ? groups : kGridX, (groups + kGridX - 1) / kGridX),
+                     grid_of(groups),
                      dim3(NW == 1 ? 256 : 64 * NW), 0, stream, d.T, d.H, d.eps, x, res, weight, sum,
                      y, yq, ys);
 }

@@ -272,8 +272,8 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // Rows past the block repeat its last row and columns past N the last column;
 // they only reach outputs that are not stored.
 //
-// Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8)
-// in contiguous runs, so that the tiles an XCD works on together share rows and
+// Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8, a
+// row of the grid being a multiple of 8) in contiguous runs, so that the tiles an XCD works on together share rows and
 // columns in its own L2: a dense run goes through groups of four row blocks
 // column by column (8192 cubed: groups of one 537 us, two 511, four 493, eight
 // 494), a grouped one block by block (16384 tokens: 426 us, in groups of four
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_tile_kernel(Q8Args a) {
   int b, ni;
   {
     const int total = nb * nt, per = (total + 7) / 8;
-    const int i = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + i;
+    const int i = static_cast<int>(workgroup() >> 3), tile = static_cast<int>(blockIdx.x & 7) * per + i;
     if (i >= per || tile >= total) return;
     constexpr int G = GROUPED ? 1 : 4;
     const int g = tile / (G * nt), r = tile - g * G * nt, gm = min(G, nb - G * g);
@@ -631,7 +631,7 @@ template <int WM, int WN, int MT, int NT, int R, bool GROUPED, bool GATHER, bool
 void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
   const long long tiles = static_cast<long long>(blocks) * cdiv(a.N, WN * NT * 32);
   hipLaunchKernelGGL((q8_tile_kernel<WM, WN, MT, NT, R, GROUPED, GATHER, SWIGLU>),
-                     dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
+                     grid_of(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, a);
 }
 
 // Which kernel.  Every one of them takes any block of a map (rows past its tile
