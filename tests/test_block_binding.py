@@ -1,0 +1,108 @@
+"""The binding's own checks for the operators of include/moe_block.h, on the CPU: host tensors stand
+for device ones and a stub for the library, so nothing is launched."""
+
+import numpy as np
+import pytest
+
+import w4_dequant_expert_amd as moe
+
+torch = pytest.importorskip("torch")
+
+F32, BF16, F16, I8 = torch.float32, torch.bfloat16, torch.float16, torch.int8
+
+
+class Stub:
+    """A library that only records which functions were called."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def stub(monkeypatch):
+    s = Stub()
+    monkeypatch.setattr(moe.moe, "_lib", s)
+    monkeypatch.setattr(moe.moe, "_device", lambda: torch.zeros(1).get_device())
+    return s
+
+
+T, H, I, E, K = 3, 64, 64, 4, 2
+ROWS = T * (K + 1)
+
+
+def calls():
+    """Every entry point: its name, the row type of the call, and its arrays (name, shape, type; None:
+    the row type)."""
+    d = moe.make_dims(T, H, I, E, K, 1)
+    r, b = moe.RouteOut(), moe.Q8Bank()
+    out = []
+    for elem in (moe.ELEM_F32, moe.ELEM_BF16, moe.ELEM_F16):
+        n = moe.NormDims(T, H, elem, 1e-6)
+        out += [
+            ("moe_add_rmsnorm", elem, lambda a, n=n: moe.moe_add_rmsnorm(n, *a, stream=0),
+             [("x", (T, H), None), ("res", (T, H), None), ("weight", (H,), F32), ("sum", (T, H), None),
+              ("y", (T, H), None), ("yq", (T, H), I8), ("ys", (T,), F32)]),
+            ("moe_add_rmsnorm_backward", elem, lambda a, n=n: moe.moe_add_rmsnorm_backward(n, *a, None, 0, stream=0),
+             [("sum", (T, H), None), ("weight", (H,), F32), ("dy", (T, H), None), ("dsum", (T, H), None),
+              ("dx", (T, H), None), ("dweight", (H,), F32)]),
+            ("moe_q8_quantize", elem, lambda a, n=n: moe.moe_q8_quantize(n, *a, stream=0),
+             [("x", (T, H), None), ("xq", (T, H), I8), ("xs", (T,), F32)]),
+            ("moe_q8_matmul", elem, lambda a, elem=elem: moe.moe_q8_matmul(moe.Q8Dims(T, I, H, elem), *a, stream=0),
+             [("xq", (T, H), I8), ("xs", (T,), F32), ("wq", (I, H), I8), ("ws", (I,), F32), ("out", (T, I), None)]),
+            ("moe_dispatch_rows", elem, lambda a, e=elem: moe.moe_dispatch_rows(d, e, a[0], r, a[1], stream=0),
+             [("x", (T, H), None), ("rows", (ROWS, H), None)]),
+            ("moe_dispatch_rows_backward", elem,
+             lambda a, e=elem: moe.moe_dispatch_rows_backward(d, e, a[0], r, a[1], stream=0),
+             [("drows", (ROWS, H), None), ("dx", (T, H), None)]),
+            ("moe_combine_rows", elem, lambda a, e=elem: moe.moe_combine_rows(d, e, a[0], r, a[1], stream=0),
+             [("rows", (ROWS, H), None), ("y", (T, H), None)]),
+            ("moe_combine_rows_backward", elem,
+             lambda a, e=elem: moe.moe_combine_rows_backward(d, e, a[0], a[1], r, a[2], a[3], stream=0),
+             [("dy", (T, H), None), ("rows", (ROWS, H), None), ("drows", (ROWS, H), None), ("dtopk_w", (T, K), F32)]),
+        ]
+    out += [
+        ("moe_q8_gate_up", None, lambda a: moe.moe_q8_gate_up(d, a[0], a[1], r, b, b, a[2], stream=0),
+         [("xq", (T, H), I8), ("xs", (T,), F32), ("h", (ROWS, I), BF16)]),
+        ("moe_q8_down", None, lambda a: moe.moe_q8_down(d, r, b, b, *a, stream=0),
+         [("hq", (ROWS, I), I8), ("hs", (ROWS,), F32), ("y_slots", (ROWS, H), BF16)]),
+    ]
+    return out
+
+
+ROW = {moe.ELEM_F32: F32, moe.ELEM_BF16: BF16, moe.ELEM_F16: F16}
+# enough bytes whatever is asked for, but another type
+WRONG = {F32: (torch.float64, torch.int32, BF16), I8: (torch.uint8, torch.int16, F32),
+         BF16: (F16, F32, I8), F16: (BF16, F32, I8)}
+
+
+def test_arrays_of_another_type_are_refused(stub):
+    for name, elem, call, arrays in calls():
+        types = [ROW[elem] if t is None else t for _, _, t in arrays]
+        good = [torch.zeros(shape, dtype=t) for (_, shape, _), t in zip(arrays, types)]
+        stub.calls.clear()
+        call(good)
+        assert stub.calls == [name]
+        for i, (arg, shape, _) in enumerate(arrays):
+            for wrong in WRONG[types[i]]:
+                bad = list(good)
+                bad[i] = torch.zeros((shape[0] * 4, *shape[1:]), dtype=wrong)
+                with pytest.raises(ValueError, match=f"^{arg}: "):
+                    call(bad)
+        assert stub.calls == [name]
+        # 16-bit rows as the integers of their bits
+        if elem in (moe.ELEM_BF16, moe.ELEM_F16):
+            call([t.view(torch.int16) if t.dtype == ROW[elem] else t for t in good])
+            call([t.view(torch.uint16) if t.dtype == ROW[elem] else t for t in good])
+            assert stub.calls == [name] * 3
+
+
+def test_arrays_that_are_not_looked_at_have_any_type(stub):
+    e = torch.empty(0, dtype=torch.float64)
+    moe.moe_q8_matmul(moe.Q8Dims(0, I, H, moe.ELEM_F32), e, e, torch.zeros((I, H), dtype=I8), torch.zeros(I), e, stream=0)
+    assert stub.calls == ["moe_q8_matmul"]

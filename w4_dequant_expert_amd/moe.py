@@ -34,6 +34,8 @@ EXPORTED = ("moe_abi_version", "moe_strerror", "moe_max_blocks", "moe_route_ws_b
 
 ELEM_F32, ELEM_BF16, ELEM_F16 = 0, 1, 2   # MOE_ELEM_*
 ELEM: dict = {}   # torch dtype -> MOE_ELEM_*, filled when the library is loaded
+# the torch types that the arrays of each kind may have, and (bytes, types) of each row type; set with ELEM
+_F32 = _I8 = _BF16 = _ROW_TYPES = ()
 
 
 class GdnDims(ctypes.Structure):
@@ -81,11 +83,13 @@ class MoeError(RuntimeError):
 
 
 _lib = None
-_torch = None   # set with _lib
+# set with _lib
+_torch = _get_device = _raw_stream = None
+_cuda_ready = False
 
 
 def lib():
-    global _lib, _torch
+    global _lib, _torch, _get_device, _raw_stream, _F32, _I8, _BF16, _ROW_TYPES
     if _lib is None:
         # torch ships its own HIP runtime.  Import it first so that loading the
         # library resolves libamdhip64.so.7 to that same runtime; loading the
@@ -165,6 +169,10 @@ def lib():
         L.moe_combine_rows_backward.restype = ctypes.c_int
         L.moe_combine_rows_backward.argtypes = [P(Dims), i32, vp, vp, P(RouteOut), vp, vp, vp]
         ELEM.update({torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.float16: ELEM_F16})
+        bits = (torch.int16, torch.uint16)
+        _F32, _I8, _BF16 = (torch.float32,), (torch.int8,), (torch.bfloat16, *bits)
+        _ROW_TYPES = ((4, _F32), (2, _BF16), (2, (torch.float16, *bits)))
+        _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _lib, _torch = L, torch
     return _lib
 
@@ -189,15 +197,30 @@ def _ptr(t):
 
 def _device() -> int:
     """The current GPU."""
+    if not _cuda_ready:
+        _init_cuda()
+    return _get_device()
+
+
+def _init_cuda():
+    global _cuda_ready
     if not _torch.cuda.is_initialized():
         _torch.cuda.init()
-    return _torch._C._cuda_getDevice()
+    _cuda_ready = True
+
+
+def _after_fork():
+    global _cuda_ready
+    _cuda_ready = False   # torch then refuses the child's use of the GPU
+
+
+os.register_at_fork(after_in_child=_after_fork)
 
 
 def _stream(stream, device=None):
     if stream is None:
         # the handle alone: building a stream object costs more than a small launch
-        return _torch._C._cuda_getCurrentRawStream(_device() if device is None else device)
+        return _raw_stream(_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -316,67 +339,74 @@ def gdn_scan_chunked(d: GdnDims, q, k, v, g, beta, state_in, state_out, o, ws, w
 
 # ------------------------------------------- around the expert layer (include/moe_block.h)
 
-_ELEM_SIZE = (4, 2, 2)
+def _row_type(elem: int):
+    """Bytes and torch types of a row type; an unknown one is refused by the C side."""
+    return _ROW_TYPES[elem] if 0 <= elem < 3 else (0, None)
 
 
-def _arg(t, nbytes: int, what: str, device: int):
+def _arg(t, nbytes: int, what: str, device: int, types=None):
     """Address of a dense array of at least nbytes on `device` (None -> NULL; raw addresses pass).
 
-    The C side cannot see sizes or strides, so tensors that are strided, too
-    small or off the current device are refused here."""
+    The C side cannot see sizes, strides or types, so tensors that are strided,
+    too small, off the current device or of another type than `types` (None:
+    any; 16-bit rows may come as the integers of their bits) are refused here.
+    The type of an array that is not looked at (nbytes 0) does not count."""
     if t is None or type(t) is int:
         return t
-    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{what}: a contiguous tensor of at least {nbytes} bytes on GPU {device} is needed, got "
+    if (t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != device or
+            (types is not None and nbytes and t.dtype not in types)):
+        raise ValueError(f"{what}: a contiguous tensor of at least {nbytes} bytes on GPU {device} is needed"
+                         f"{'' if types is None else ' of ' + ' or '.join(map(str, types))}, got "
                          f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
-
-
-def _elem_bytes(elem: int) -> int:
-    return _ELEM_SIZE[elem] if 0 <= elem < 3 else 0   # an unknown type is refused by the C side
 
 
 def moe_add_rmsnorm(d: NormDims, x, res, weight, sum, y, yq=None, ys=None, stream=None):
     """Residual addition and RMS norm (any of res, sum, y, yq with ys may be None)."""
     dev = _device()
     n = d.T * d.H
-    row = n * _elem_bytes(d.type)
-    _check(lib().moe_add_rmsnorm(ctypes.byref(d), _arg(x, row, "x", dev), _arg(res, row, "res", dev),
-                                 _arg(weight, 4 * d.H, "weight", dev), _arg(sum, row, "sum", dev),
-                                 _arg(y, row, "y", dev), _arg(yq, n, "yq", dev), _arg(ys, 4 * d.T, "ys", dev),
-                                 _stream(stream, dev)), "moe_add_rmsnorm")
+    size, typ = _row_type(d.type)
+    row = n * size
+    _check(_lib.moe_add_rmsnorm(d, _arg(x, row, "x", dev, typ), _arg(res, row, "res", dev, typ),
+                                _arg(weight, 4 * d.H, "weight", dev, _F32), _arg(sum, row, "sum", dev, typ),
+                                _arg(y, row, "y", dev, typ), _arg(yq, n, "yq", dev, _I8),
+                                _arg(ys, 4 * d.T, "ys", dev, _F32), _stream(stream, dev)), "moe_add_rmsnorm")
 
 
 def moe_add_rmsnorm_backward_ws_bytes(d: NormDims) -> int:
-    return lib().moe_add_rmsnorm_backward_ws_bytes(ctypes.byref(d))
+    return _lib.moe_add_rmsnorm_backward_ws_bytes(d)
 
 
 def moe_add_rmsnorm_backward(d: NormDims, sum, weight, dy, dsum, dx, dweight, ws, ws_bytes: int,
                              stream=None):
     """Gradients of moe_add_rmsnorm (dsum and dweight may be None)."""
     dev = _device()
-    row = d.T * d.H * _elem_bytes(d.type)
-    _check(lib().moe_add_rmsnorm_backward(
-        ctypes.byref(d), _arg(sum, row, "sum", dev), _arg(weight, 4 * d.H, "weight", dev), _arg(dy, row, "dy", dev),
-        _arg(dsum, row, "dsum", dev), _arg(dx, row, "dx", dev), _arg(dweight, 4 * d.H, "dweight", dev),
-        _arg(ws, ws_bytes, "ws", dev), ws_bytes, _stream(stream, dev)), "moe_add_rmsnorm_backward")
+    size, typ = _row_type(d.type)
+    row = d.T * d.H * size
+    _check(_lib.moe_add_rmsnorm_backward(
+        d, _arg(sum, row, "sum", dev, typ), _arg(weight, 4 * d.H, "weight", dev, _F32),
+        _arg(dy, row, "dy", dev, typ), _arg(dsum, row, "dsum", dev, typ), _arg(dx, row, "dx", dev, typ),
+        _arg(dweight, 4 * d.H, "dweight", dev, _F32), _arg(ws, ws_bytes, "ws", dev), ws_bytes,
+        _stream(stream, dev)), "moe_add_rmsnorm_backward")
 
 
 def moe_q8_quantize(d: NormDims, x, xq, xs, stream=None):
     """Rows to int8 with a scale per row."""
     dev = _device()
     n = d.T * d.H
-    _check(lib().moe_q8_quantize(ctypes.byref(d), _arg(x, n * _elem_bytes(d.type), "x", dev),
-                                 _arg(xq, n, "xq", dev), _arg(xs, 4 * d.T, "xs", dev), _stream(stream, dev)),
+    size, typ = _row_type(d.type)
+    _check(_lib.moe_q8_quantize(d, _arg(x, n * size, "x", dev, typ), _arg(xq, n, "xq", dev, _I8),
+                                _arg(xs, 4 * d.T, "xs", dev, _F32), _stream(stream, dev)),
            "moe_q8_quantize")
 
 
 def moe_q8_matmul(d: Q8Dims, xq, xs, wq, ws, out, stream=None):
     """Dense product of 8-bit integers with token and channel scales."""
     dev = _device()
-    _check(lib().moe_q8_matmul(ctypes.byref(d), _arg(xq, d.M * d.K, "xq", dev), _arg(xs, 4 * d.M, "xs", dev),
-                               _arg(wq, d.N * d.K, "wq", dev), _arg(ws, 4 * d.N, "ws", dev),
-                               _arg(out, d.M * d.N * _elem_bytes(d.type), "out", dev), _stream(stream, dev)),
+    size, typ = _row_type(d.type)
+    _check(_lib.moe_q8_matmul(d, _arg(xq, d.M * d.K, "xq", dev, _I8), _arg(xs, 4 * d.M, "xs", dev, _F32),
+                              _arg(wq, d.N * d.K, "wq", dev, _I8), _arg(ws, 4 * d.N, "ws", dev, _F32),
+                              _arg(out, d.M * d.N * size, "out", dev, typ), _stream(stream, dev)),
            "moe_q8_matmul")
 
 
@@ -386,46 +416,47 @@ def _rows_of(d: Dims) -> int:
 
 def moe_q8_gate_up(d: Dims, xq, xs, out: RouteOut, routed: Q8Bank, shared, h, stream=None):
     dev = _device()
-    _check(lib().moe_q8_gate_up(ctypes.byref(d), _arg(xq, d.T * d.H, "xq", dev), _arg(xs, 4 * d.T, "xs", dev),
-                                ctypes.byref(out), ctypes.byref(routed),
-                                ctypes.byref(shared) if shared is not None else None,
-                                _arg(h, 2 * _rows_of(d) * d.I, "h", dev), _stream(stream, dev)),
+    _check(_lib.moe_q8_gate_up(d, _arg(xq, d.T * d.H, "xq", dev, _I8), _arg(xs, 4 * d.T, "xs", dev, _F32),
+                               out, routed, shared,
+                               _arg(h, 2 * _rows_of(d) * d.I, "h", dev, _BF16), _stream(stream, dev)),
            "moe_q8_gate_up")
 
 
 def moe_q8_down(d: Dims, out: RouteOut, routed: Q8Bank, shared, hq, hs, y_slots, stream=None):
     dev = _device()
     rows = _rows_of(d)
-    _check(lib().moe_q8_down(ctypes.byref(d), ctypes.byref(out), ctypes.byref(routed),
-                             ctypes.byref(shared) if shared is not None else None,
-                             _arg(hq, rows * d.I, "hq", dev), _arg(hs, 4 * rows, "hs", dev),
-                             _arg(y_slots, 2 * rows * d.H, "y_slots", dev), _stream(stream, dev)),
+    _check(_lib.moe_q8_down(d, out, routed, shared,
+                            _arg(hq, rows * d.I, "hq", dev, _I8), _arg(hs, 4 * rows, "hs", dev, _F32),
+                            _arg(y_slots, 2 * rows * d.H, "y_slots", dev, _BF16), _stream(stream, dev)),
            "moe_q8_down")
 
 
 def moe_dispatch_rows(d: Dims, elem: int, x, out: RouteOut, rows, stream=None):
     """Token rows into moe_route's order (elem: one of ELEM_*)."""
     dev = _device()
-    e = _elem_bytes(elem) * d.H
-    _check(lib().moe_dispatch_rows(ctypes.byref(d), elem, _arg(x, d.T * e, "x", dev), ctypes.byref(out),
-                                   _arg(rows, _rows_of(d) * e, "rows", dev), _stream(stream, dev)),
+    size, typ = _row_type(elem)
+    e = size * d.H
+    _check(_lib.moe_dispatch_rows(d, elem, _arg(x, d.T * e, "x", dev, typ), out,
+                                  _arg(rows, _rows_of(d) * e, "rows", dev, typ), _stream(stream, dev)),
            "moe_dispatch_rows")
 
 
 def moe_dispatch_rows_backward(d: Dims, elem: int, drows, out: RouteOut, dx, stream=None):
     dev = _device()
-    e = _elem_bytes(elem) * d.H
-    _check(lib().moe_dispatch_rows_backward(ctypes.byref(d), elem, _arg(drows, _rows_of(d) * e, "drows", dev),
-                                            ctypes.byref(out), _arg(dx, d.T * e, "dx", dev),
-                                            _stream(stream, dev)), "moe_dispatch_rows_backward")
+    size, typ = _row_type(elem)
+    e = size * d.H
+    _check(_lib.moe_dispatch_rows_backward(d, elem, _arg(drows, _rows_of(d) * e, "drows", dev, typ),
+                                           out, _arg(dx, d.T * e, "dx", dev, typ),
+                                           _stream(stream, dev)), "moe_dispatch_rows_backward")
 
 
 def moe_combine_rows(d: Dims, elem: int, rows, out: RouteOut, y, stream=None):
     """moe_combine for any row type."""
     dev = _device()
-    e = _elem_bytes(elem) * d.H
-    _check(lib().moe_combine_rows(ctypes.byref(d), elem, _arg(rows, _rows_of(d) * e, "rows", dev),
-                                  ctypes.byref(out), _arg(y, d.T * e, "y", dev), _stream(stream, dev)),
+    size, typ = _row_type(elem)
+    e = size * d.H
+    _check(_lib.moe_combine_rows(d, elem, _arg(rows, _rows_of(d) * e, "rows", dev, typ),
+                                 out, _arg(y, d.T * e, "y", dev, typ), _stream(stream, dev)),
            "moe_combine_rows")
 
 
@@ -433,12 +464,13 @@ def moe_combine_rows_backward(d: Dims, elem: int, dy, rows, out: RouteOut, drows
                               stream=None):
     """Gradients of the combine (dtopk_w None: rows is not read and may be None)."""
     dev = _device()
-    e = _elem_bytes(elem) * d.H
-    _check(lib().moe_combine_rows_backward(ctypes.byref(d), elem, _arg(dy, d.T * e, "dy", dev),
-                                           _arg(rows, _rows_of(d) * e, "rows", dev), ctypes.byref(out),
-                                           _arg(drows, _rows_of(d) * e, "drows", dev),
-                                           _arg(dtopk_w, 4 * d.T * d.k, "dtopk_w", dev),
-                                           _stream(stream, dev)), "moe_combine_rows_backward")
+    size, typ = _row_type(elem)
+    e = size * d.H
+    _check(_lib.moe_combine_rows_backward(d, elem, _arg(dy, d.T * e, "dy", dev, typ),
+                                          _arg(rows, _rows_of(d) * e, "rows", dev, typ), out,
+                                          _arg(drows, _rows_of(d) * e, "drows", dev, typ),
+                                          _arg(dtopk_w, 4 * d.T * d.k, "dtopk_w", dev, _F32),
+                                          _stream(stream, dev)), "moe_combine_rows_backward")
 
 
 # --------------------------------------------------------------------- device buffers
