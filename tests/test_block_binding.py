@@ -106,3 +106,48 @@ def test_arrays_that_are_not_looked_at_have_any_type(stub):
     e = torch.empty(0, dtype=torch.float64)
     moe.moe_q8_matmul(moe.Q8Dims(0, I, H, moe.ELEM_F32), e, e, torch.zeros((I, H), dtype=I8), torch.zeros(I), e, stream=0)
     assert stub.calls == ["moe_q8_matmul"]
+
+
+# ------------------------------------------------------------------------------- the 8-bit layer
+
+def q8_bank(n, h=H, i=I):
+    """A bank on the host, made without the quantiser."""
+    b = moe.DeviceBankQ8.__new__(moe.DeviceBankQ8)
+    b.n, b.H, b.I = n, h, i
+    b.t = {"gu": torch.zeros((n, 2 * i, h), dtype=I8), "gu_s": torch.zeros((n, 2 * i)),
+           "dn": torch.zeros((n, h, i), dtype=I8), "dn_s": torch.zeros((n, h))}
+    b.c = moe.Q8Bank(*[b.t[k].data_ptr() for k in ("gu", "gu_s", "dn", "dn_s")])
+    return b
+
+
+def q8_layer(routed, shared, n_shared=1, **kw):
+    return moe.Q8MoeLayer(H, I, E, K, n_shared, routed, shared, np.zeros((H, E), np.float32), T_max=8, device="cpu", **kw)
+
+
+def test_layer_refuses_banks_that_are_not_its_own_size(stub):
+    layer = q8_layer(q8_bank(E), q8_bank(1))
+    x, y = torch.zeros((T, H), dtype=BF16), torch.zeros((T, H), dtype=BF16)
+    layer.forward(x, y, stream=0)
+    layer.forward(x, y, routed=q8_bank(E + 1), shared=q8_bank(2), stream=0)   # more experts than are read
+    assert stub.calls.count("moe_q8_gate_up") == 2 and stub.calls.count("moe_q8_down") == 2
+    stub.calls.clear()
+    d = layer.dims(T)
+    w4 = moe.DeviceBank.from_tensors({"gu": torch.zeros(1), "dn": torch.zeros(1)}, E, H, I)
+    for routed in (q8_bank(E - 1), q8_bank(E, h=H + 64), q8_bank(E, i=I - 32), q8_bank(E, h=H // 2), w4):
+        with pytest.raises(ValueError, match="^routed: "):
+            q8_layer(routed, q8_bank(1))
+        with pytest.raises(ValueError, match="^routed: "):
+            layer._gate_up_quantised(d, routed=routed, stream=0)
+        with pytest.raises(ValueError, match="^routed: "):
+            layer.down(d, routed=routed, stream=0)
+    for shared in (q8_bank(0), q8_bank(1, h=H + 64), q8_bank(1, i=2 * I)):
+        with pytest.raises(ValueError, match="^shared: "):
+            q8_layer(q8_bank(E), shared)
+        with pytest.raises(ValueError, match="^shared: "):
+            layer.down(d, shared=shared, stream=0)
+    assert not {"moe_q8_gate_up", "moe_q8_down"} & set(stub.calls)
+    q8_layer(q8_bank(E), None, n_shared=0)
+    # replaced on the layer itself
+    layer.routed = q8_bank(1)
+    with pytest.raises(ValueError, match="^routed: "):
+        layer.forward(x, y, stream=0)

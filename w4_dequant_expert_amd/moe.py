@@ -572,6 +572,9 @@ class DeviceBankQ8:
     def nbytes(self) -> int:
         return sum(v.numel() * v.element_size() for v in self.t.values())
 
+    def __repr__(self):
+        return f"DeviceBankQ8 of {self.n} experts, H {self.H}, I {self.I} on {self.t['gu'].device}"
+
 
 class RouteTables:
     """Device arrays for every routing output of one layer call of up to T tokens."""
@@ -706,11 +709,13 @@ class MoeLayer:
 class Q8MoeLayer(MoeLayer):
     """The same layer with 8-bit banks (DeviceBankQ8): routing and combine as in
     MoeLayer, the products in 8-bit integers.  gate_up, and so forward, quantises
-    the tokens itself; forward_residual gets them from the norm."""
+    the tokens itself; forward_residual gets them from the norm.  A bank of other
+    sizes than the layer's, or with fewer experts, is refused."""
 
     def __init__(self, *args, device="cuda", **kw):
         import torch
         super().__init__(*args, device=device, **kw)
+        self._banks()
         rows = self.h.shape[0]
         self.xq = torch.empty((self.T_max, self.H), dtype=torch.int8, device=device)
         self.xs = torch.empty((self.T_max,), dtype=torch.float32, device=device)
@@ -721,18 +726,25 @@ class Q8MoeLayer(MoeLayer):
         moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
         self._gate_up_quantised(d, routed, shared, stream)
 
+    def _banks(self, routed=None, shared=None):
+        """The C structs of the banks of a call (None: the layer's own); the kernels read them by the
+        layer's sizes."""
+        out = []
+        for what, bank, n in (("routed", routed or self.routed, self.E), ("shared", shared or self.shared, 1)):
+            if bank is not None and not (isinstance(bank, DeviceBankQ8) and bank.n >= n and bank.H == self.H and
+                                         bank.I == self.I and bank.t["gu"].device == self.h.device):
+                raise ValueError(f"{what}: a DeviceBankQ8 of {n} experts, H {self.H}, I {self.I} on {self.h.device} "
+                                 f"is needed, got {bank}")
+            out.append(None if bank is None else bank.c)
+        return out
+
     def _gate_up_quantised(self, d, routed=None, shared=None, stream=None):
-        r = routed or self.routed
-        s = shared or self.shared
-        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, r.c, s.c if s is not None else None, self.h,
-                       stream)
+        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, *self._banks(routed, shared), self.h, stream)
 
     def down(self, d, routed=None, shared=None, stream=None):
-        r = routed or self.routed
-        s = shared or self.shared
+        banks = self._banks(routed, shared)
         moe_q8_quantize(NormDims(_rows_of(d), self.I, ELEM_BF16, 0.0), self.h, self.hq, self.hs, stream)
-        moe_q8_down(d, self.rt.c, r.c, s.c if s is not None else None, self.hq, self.hs, self.y_slots,
-                    stream)
+        moe_q8_down(d, self.rt.c, *banks, self.hq, self.hs, self.y_slots, stream)
 
     def ffn(self, d, x, routed=None, shared=None, stream=None):
         self.gate_up(d, x, routed, shared, stream)
