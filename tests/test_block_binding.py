@@ -151,3 +151,9 @@ def test_layer_refuses_banks_that_are_not_its_own_size(stub):
     layer.routed = q8_bank(1)
     with pytest.raises(ValueError, match="^routed: "):
         layer.forward(x, y, stream=0)
+
+
+def test_bank_refuses_an_odd_count_of_gate_and_up_rows(stub):
+    with pytest.raises(ValueError):
+        moe.DeviceBankQ8(torch.zeros((2, 129, 64)), torch.zeros((2, 64, 64)))
+    assert not stub.calls

@@ -538,6 +538,8 @@ class DeviceBankQ8:
     def __init__(self, gu, dn):
         n, two_i, H = gu.shape
         self.n, self.H, self.I = n, H, two_i // 2
+        if two_i % 2:
+            raise ValueError(f"gu has {two_i} rows an expert: gate and up rows come in pairs")
         if dn.shape != (n, H, self.I):
             raise ValueError(f"dn has shape {tuple(dn.shape)}, not {(n, H, self.I)}")
         gq, gs = self._quantize(gu)
