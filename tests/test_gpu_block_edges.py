@@ -87,3 +87,19 @@ def test_a_launch_of_more_than_2_32_threads():
         got = y[torch.from_numpy(m).cuda()].double().cpu().numpy()
         assert (np.abs(got - want) <= (2.0 ** -8 + 3 * ref.EPS32) * np.abs(want) * (1 + 1e-6) + 1e-37).all()
     assert int(tab.status.item()) == 0
+
+
+# ------------------------------------------------------------------------------------- the 8-bit bank
+
+def test_a_bank_is_complete_when_it_is_made():
+    """Its weights may be used on any stream from then on, as those of a 4-bit bank."""
+    from synth import build_config
+    c = build_config("tiny16")
+    a = torch.randn((4096, 4096), device="cuda")
+    gu, dn = torch.randn((8, 1024, 2048), device="cuda"), torch.randn((8, 2048, 512), device="cuda")
+    for make in (lambda: moe.DeviceBankQ8(gu, dn), lambda: moe.DeviceBankQ8.from_w4(c["routed"]),
+                 lambda: moe.DeviceBank(c["routed"])):
+        for _ in range(8):
+            a = torch.mm(a, a).mul_(1e-3)   # work that the bank's own waits behind
+        make()
+        assert torch.cuda.current_stream().query()

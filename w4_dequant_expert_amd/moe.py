@@ -536,6 +536,7 @@ class DeviceBankQ8:
     """
 
     def __init__(self, gu, dn):
+        import torch
         n, two_i, H = gu.shape
         self.n, self.H, self.I = n, H, two_i // 2
         if two_i % 2:
@@ -544,6 +545,7 @@ class DeviceBankQ8:
             raise ValueError(f"dn has shape {tuple(dn.shape)}, not {(n, H, self.I)}")
         gq, gs = self._quantize(gu)
         dq, ds = self._quantize(dn)
+        torch.cuda.current_stream().synchronize()   # the bank may be used on any stream from here on
         self.t = {"gu": gq, "gu_s": gs, "dn": dq, "dn_s": ds}
         self.c = Q8Bank(*[self.t[k].data_ptr() for k in ("gu", "gu_s", "dn", "dn_s")])
 
@@ -557,7 +559,6 @@ class DeviceBankQ8:
             n, rows, half_k = q.shape
             w = torch.empty((n, rows, 2 * half_k), dtype=torch.bfloat16, device=device)
             moe_w4_dequant(n * rows, 2 * half_k, q, s, b, w)
-            torch.cuda.current_stream().synchronize()
             out.append(w)
         return cls(*out)
 
