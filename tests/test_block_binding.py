@@ -157,3 +157,33 @@ def test_bank_refuses_an_odd_count_of_gate_and_up_rows(stub):
     with pytest.raises(ValueError):
         moe.DeviceBankQ8(torch.zeros((2, 129, 64)), torch.zeros((2, 64, 64)))
     assert not stub.calls
+
+
+def checkpoint(n=2):
+    z = lambda rows, k, t: np.zeros((n, rows, k), t)
+    return dict(gu_q=z(2 * I, H // 2, np.uint8), gu_s=z(2 * I, H // 64, np.uint16), gu_b=z(2 * I, H // 64, np.uint16),
+                dn_q=z(H, I // 2, np.uint8), dn_s=z(H, I // 64, np.uint16), dn_b=z(H, I // 64, np.uint16))
+
+
+def test_bank_from_4_bits_checks_what_the_dequantiser_gets(stub, monkeypatch):
+    """Arrays off the current device, with too few scales or of another type never reach it."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), dict(cuda_stream=0, synchronize=lambda s: None))())
+    monkeypatch.setattr(moe.moe, "_raw_stream", lambda device: 0)
+    moe.DeviceBankQ8.from_w4(checkpoint(), device="cpu")
+    assert stub.calls == ["moe_w4_dequant"] * 2 + ["moe_q8_quantize"] * 2
+    stub.calls.clear()
+    bad = []
+    for half, field in (("gu", "s"), ("gu", "b"), ("dn", "s"), ("dn", "b")):
+        c = checkpoint()
+        c[f"{half}_{field}"] = c[f"{half}_{field}"][:1]
+        bad.append((f"{half}_{field}", c))
+        c = checkpoint()
+        c[f"{half}_{field}"] = c[f"{half}_{field}"].astype(np.float32)
+        bad.append((f"{half}_{field}", c))
+    for what, c in bad:
+        with pytest.raises(ValueError, match=f"^{what}: "):
+            moe.DeviceBankQ8.from_w4(c, device="cpu")
+    monkeypatch.setattr(moe.moe, "_device", lambda: 0)
+    with pytest.raises(ValueError, match="^gu_q: "):
+        moe.DeviceBankQ8.from_w4(checkpoint(), device="cpu")
+    assert stub.calls.count("moe_w4_dequant") == 4    # the gate/up half of the four whose down half was wrong

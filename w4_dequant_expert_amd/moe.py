@@ -558,6 +558,11 @@ class DeviceBankQ8:
             q, s, b = (_dev(bank[f"{half}_{p}"], device) for p in "qsb")
             n, rows, half_k = q.shape
             w = torch.empty((n, rows, 2 * half_k), dtype=torch.bfloat16, device=device)
+            # what the dequantiser reads and writes lies on the current device, and is all there
+            dev, groups = _device(), n * rows * (half_k // 32)
+            _arg(q, 1, f"{half}_q", dev, (torch.uint8,))
+            _arg(s, 2 * groups, f"{half}_s", dev, _BF16)
+            _arg(b, 2 * groups, f"{half}_b", dev, _BF16)
             moe_w4_dequant(n * rows, 2 * half_k, q, s, b, w)
             out.append(w)
         return cls(*out)
