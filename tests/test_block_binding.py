@@ -187,3 +187,30 @@ def test_bank_from_4_bits_checks_what_the_dequantiser_gets(stub, monkeypatch):
     with pytest.raises(ValueError, match="^gu_q: "):
         moe.DeviceBankQ8.from_w4(checkpoint(), device="cpu")
     assert stub.calls.count("moe_w4_dequant") == 4    # the gate/up half of the four whose down half was wrong
+
+
+def test_widths_that_the_quantiser_does_not_take_are_refused_at_construction(stub):
+    wide = moe.NORM_MAX_H + 64
+    for h, i in ((wide, I), (H, wide)):
+        with pytest.raises(ValueError, match="quantised at up to"):
+            moe.DeviceBankQ8(torch.zeros((1, 2 * i, h)), torch.zeros((1, h, i)))
+        with pytest.raises(ValueError, match="quantised at up to"):
+            moe.Q8MoeLayer(h, i, E, K, 0, None, None, None, T_max=8, device="cpu")
+    assert not stub.calls
+
+
+def test_layer_quantises_more_rows_than_one_call_takes(stub, monkeypatch):
+    """h goes to the quantiser in runs of at most its row limit (a small one here)."""
+    monkeypatch.setattr(moe.moe, "NORM_MAX_T", 7)
+    seen = []
+    monkeypatch.setattr(moe.moe, "moe_q8_quantize", lambda d, x, q, s, stream=None: seen.append(
+        (d.T, x.data_ptr(), q.data_ptr(), s.data_ptr())))
+    layer = q8_layer(q8_bank(E), q8_bank(1))
+    for t in (0, 1, 2, 3, 5, 7, 8):
+        seen.clear()
+        layer.down(layer.dims(t), stream=0)
+        rows = t * (K + 1)
+        assert [n for n, *_ in seen] == ([7] * (rows // 7) + [rows % 7] * (rows % 7 > 0) or [0])
+        for j, (_, x, q, s) in enumerate(seen):
+            assert (x, q, s) == (layer.h.data_ptr() + 14 * j * I, layer.hq.data_ptr() + 7 * j * I,
+                                 layer.hs.data_ptr() + 28 * j)

@@ -103,3 +103,28 @@ def test_a_bank_is_complete_when_it_is_made():
             a = torch.mm(a, a).mul_(1e-3)   # work that the bank's own waits behind
         make()
         assert torch.cuda.current_stream().query()
+
+
+def test_layer_of_more_rows_than_the_quantiser_takes_at_once():
+    """A million tokens with sixteen experts and a shared one each: 17 * 2^20 rows between the products.
+    Tokens repeat with a period, so every period has the first one's outputs."""
+    H, I, E, k, T, period = 64, 64, 16, 16, 1 << 20, 1 << 14
+    print(f"layer of {T * (k + 1)} rows", flush=True)
+    rng = np.random.default_rng(17)
+    gu = torch.from_numpy((rng.standard_normal((E + 1, 2 * I, H)) / 8).astype(np.float32)).cuda()
+    dn = torch.from_numpy((rng.standard_normal((E + 1, H, I)) / 8).astype(np.float32)).cuda()
+    wr = rng.standard_normal((H, E)).astype(np.float32)
+    routed, shared = moe.DeviceBankQ8(gu[:E], dn[:E]), moe.DeviceBankQ8(gu[E:], dn[E:])
+    x = torch.from_numpy(rng.standard_normal((period, H)).astype(np.float32)).cuda().to(torch.bfloat16)
+    small = moe.Q8MoeLayer(H, I, E, k, 1, routed, shared, wr, None, T_max=period, tile_m_max=256)
+    want = torch.empty_like(x)
+    small.forward(x, want)
+    layer = moe.Q8MoeLayer(H, I, E, k, 1, routed, shared, wr, None, T_max=T, tile_m_max=256)
+    assert T * (k + 1) > moe.NORM_MAX_T
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    layer.forward(x.repeat(T // period, 1), y)
+    torch.cuda.synchronize()
+    assert int(layer.rt.status.item()) == 0 and int(small.rt.status.item()) == 0
+    assert bool(torch.isfinite(want.float()).all()) and float(want.abs().max()) > 0
+    # the router scores, and so every weight and output, are defined bit for bit
+    assert bool((y.view(T // period, period, H) == want).all())

@@ -33,6 +33,7 @@ EXPORTED = ("moe_abi_version", "moe_strerror", "moe_max_blocks", "moe_route_ws_b
             "moe_dispatch_rows_backward", "moe_combine_rows", "moe_combine_rows_backward")
 
 ELEM_F32, ELEM_BF16, ELEM_F16 = 0, 1, 2   # MOE_ELEM_*
+NORM_MAX_T, NORM_MAX_H = 1 << 24, 16384   # moe_norm_dims
 ELEM: dict = {}   # torch dtype -> MOE_ELEM_*, filled when the library is loaded
 # the torch types that the arrays of each kind may have, and (bytes, types) of each row type; set with ELEM
 _F32 = _I8 = _BF16 = _ROW_TYPES = ()
@@ -528,11 +529,17 @@ class DeviceBank:
         return sum(v.numel() * v.element_size() for v in self.t.values())
 
 
+def _check_q8_widths(H, I):
+    if not (0 < H <= NORM_MAX_H and 0 < I <= NORM_MAX_H):
+        raise ValueError(f"H={H}, I={I}: rows are quantised at up to {NORM_MAX_H} elements")
+
+
 class DeviceBankQ8:
     """An expert bank resident in device memory in 8 bits (moe_q8_bank).
 
     gu [n][2I][H] (gate rows, then up rows) and dn [n][H][I] are float device
-    tensors; each output channel is quantised once by moe_q8_quantize.
+    tensors, H and I at most NORM_MAX_H; each output channel is quantised once by
+    moe_q8_quantize.
     """
 
     def __init__(self, gu, dn):
@@ -541,6 +548,7 @@ class DeviceBankQ8:
         self.n, self.H, self.I = n, H, two_i // 2
         if two_i % 2:
             raise ValueError(f"gu has {two_i} rows an expert: gate and up rows come in pairs")
+        _check_q8_widths(H, self.I)
         if dn.shape != (n, H, self.I):
             raise ValueError(f"dn has shape {tuple(dn.shape)}, not {(n, H, self.I)}")
         gq, gs = self._quantize(gu)
@@ -707,7 +715,8 @@ class MoeLayer:
 
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
         """The layer with what stands in front of it: res += x in place, then
-        the layer on the RMS norm of the sum (bfloat16 rows, one norm call)."""
+        the layer on the RMS norm of the sum (bfloat16 rows of at most NORM_MAX_H
+        elements, one norm call)."""
         d = self.dims(x.shape[0])
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         stream=stream)
@@ -717,12 +726,14 @@ class MoeLayer:
 class Q8MoeLayer(MoeLayer):
     """The same layer with 8-bit banks (DeviceBankQ8): routing and combine as in
     MoeLayer, the products in 8-bit integers.  gate_up, and so forward, quantises
-    the tokens itself; forward_residual gets them from the norm.  A bank of other
-    sizes than the layer's, or with fewer experts, is refused."""
+    the tokens itself; forward_residual gets them from the norm.  H and I are at
+    most NORM_MAX_H.  A bank of other sizes than the layer's, or with fewer
+    experts, is refused."""
 
-    def __init__(self, *args, device="cuda", **kw):
+    def __init__(self, H, I, *args, device="cuda", **kw):
         import torch
-        super().__init__(*args, device=device, **kw)
+        _check_q8_widths(H, I)
+        super().__init__(H, I, *args, device=device, **kw)
         self._banks()
         rows = self.h.shape[0]
         self.xq = torch.empty((self.T_max, self.H), dtype=torch.int8, device=device)
@@ -751,7 +762,11 @@ class Q8MoeLayer(MoeLayer):
 
     def down(self, d, routed=None, shared=None, stream=None):
         banks = self._banks(routed, shared)
-        moe_q8_quantize(NormDims(_rows_of(d), self.I, ELEM_BF16, 0.0), self.h, self.hq, self.hs, stream)
+        rows = _rows_of(d)
+        moe_q8_quantize(NormDims(min(rows, NORM_MAX_T), self.I, ELEM_BF16, 0.0), self.h, self.hq, self.hs, stream)
+        for lo in range(NORM_MAX_T, rows, NORM_MAX_T):   # up to 33 * 2^20 rows
+            moe_q8_quantize(NormDims(min(rows - lo, NORM_MAX_T), self.I, ELEM_BF16, 0.0), self.h[lo:], self.hq[lo:],
+                            self.hs[lo:], stream)
         moe_q8_down(d, self.rt.c, *banks, self.hq, self.hs, self.y_slots, stream)
 
     def ffn(self, d, x, routed=None, shared=None, stream=None):
