@@ -214,3 +214,29 @@ def test_layer_quantises_more_rows_than_one_call_takes(stub, monkeypatch):
         for j, (_, x, q, s) in enumerate(seen):
             assert (x, q, s) == (layer.h.data_ptr() + 14 * j * I, layer.hq.data_ptr() + 7 * j * I,
                                  layer.hs.data_ptr() + 28 * j)
+
+
+def test_banks_of_more_rows_than_one_call_takes_go_in_pieces(stub, monkeypatch):
+    """2^24 rows for the quantiser, 2^32 groups of eight weights for the dequantiser; and a checkpoint in
+    pieces gets the addresses of its pieces."""
+    pieces = moe.moe._pieces
+    for n, rows, k in ((256, 1024, 2048), (256, 2 ** 17, 64), (1024, 2 ** 15 + 128, 64), (5, 2 ** 17, 16384),
+                       (256, 4096, 16384), (1, 64, 64), (0, 64, 64)):
+        p = pieces(n, rows, k)
+        assert [e for s in p for e in range(s.start, s.stop)] == list(range(n))
+        for s in p:
+            m = s.stop - s.start
+            assert m >= 1 and m * rows <= 2 ** 24 and (m * rows * (k // 8) + 255) // 256 * 256 < 2 ** 32
+    assert len(pieces(256, 1024, 2048)) == 1 and len(pieces(256, 2 ** 17, 64)) == 2
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("S", (), dict(synchronize=lambda s: None))())
+    monkeypatch.setattr(moe.moe, "NORM_MAX_T", 2 * 2 * I)   # two experts' gate and up rows
+    seen = []
+    monkeypatch.setattr(moe.moe, "moe_w4_dequant", lambda r, k, q, s, b, w: seen.append((r, q.shape, s.shape, w.shape)))
+    monkeypatch.setattr(moe.moe, "moe_q8_quantize", lambda d, w, q, s: seen.append((d.T, w.shape, q.shape, s.shape)))
+    moe.DeviceBankQ8.from_w4(checkpoint(5), device="cpu")
+    two_i = 2 * I
+    want = [(m * two_i, (m, two_i, H // 2), (m, two_i, 1), (m, two_i, H)) for m in (2, 2, 1)]
+    want += [(m * H, (m, H, I // 2), (m, H, 1), (m, H, I)) for m in (4, 1)]
+    want += [(m * two_i, (m, two_i, H), (m, two_i, H), (m, two_i)) for m in (2, 2, 1)]
+    want += [(m * H, (m, H, I), (m, H, I), (m, H)) for m in (4, 1)]
+    assert seen == want

@@ -128,3 +128,14 @@ def test_layer_of_more_rows_than_the_quantiser_takes_at_once():
     assert bool(torch.isfinite(want.float()).all()) and float(want.abs().max()) > 0
     # the router scores, and so every weight and output, are defined bit for bit
     assert bool((y.view(T // period, period, H) == want).all())
+
+
+def test_bank_of_more_rows_than_the_quantiser_takes_at_once():
+    """Three experts of 2^23 gate and up rows: two calls, and every row as by itself."""
+    n, rows, H = 3, 1 << 23, 8
+    gu = torch.randn((n, rows, H), device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(torch.bfloat16)
+    q, s = moe.DeviceBankQ8._quantize(gu)
+    one, ones = torch.empty_like(q[0]), torch.empty_like(s[0])
+    for e in range(n):
+        moe.moe_q8_quantize(moe.NormDims(rows, H, moe.ELEM_BF16, 0.0), gu[e], one, ones)
+        assert torch.equal(q[e], one) and torch.equal(s[e], ones)

@@ -534,6 +534,13 @@ def _check_q8_widths(H, I):
         raise ValueError(f"H={H}, I={I}: rows are quantised at up to {NORM_MAX_H} elements")
 
 
+def _pieces(n: int, rows: int, K: int):
+    """Slices of n matrices of rows x K that one call takes: the quantiser 2^24 rows, the dequantiser
+    fewer than 2^32 groups of eight weights (a thread each, 256 a workgroup)."""
+    step = max(1, min(NORM_MAX_T // rows, (2 ** 35 - 2 ** 11) // (rows * K)))
+    return [slice(lo, min(lo + step, n)) for lo in range(0, n, step)]
+
+
 class DeviceBankQ8:
     """An expert bank resident in device memory in 8 bits (moe_q8_bank).
 
@@ -571,18 +578,20 @@ class DeviceBankQ8:
             _arg(q, 1, f"{half}_q", dev, (torch.uint8,))
             _arg(s, 2 * groups, f"{half}_s", dev, _BF16)
             _arg(b, 2 * groups, f"{half}_b", dev, _BF16)
-            moe_w4_dequant(n * rows, 2 * half_k, q, s, b, w)
+            for e in _pieces(n, rows, 2 * half_k):
+                moe_w4_dequant(w[e].shape[0] * rows, 2 * half_k, q[e], s[e], b[e], w[e])
             out.append(w)
         return cls(*out)
 
     @staticmethod
     def _quantize(w):
         import torch
-        w = w.contiguous()
         n, rows, K = w.shape
         q = torch.empty((n, rows, K), dtype=torch.int8, device=w.device)
         s = torch.empty((n, rows), dtype=torch.float32, device=w.device)
-        moe_q8_quantize(NormDims(n * rows, K, ELEM[w.dtype], 0.0), w, q, s)
+        for e in _pieces(n, rows, K):
+            part = w[e].contiguous()
+            moe_q8_quantize(NormDims(part.shape[0] * rows, K, ELEM[w.dtype], 0.0), part, q[e], s[e])
         return q, s
 
     def nbytes(self) -> int:
