@@ -240,3 +240,12 @@ def test_banks_of_more_rows_than_one_call_takes_go_in_pieces(stub, monkeypatch):
     want += [(m * two_i, (m, two_i, H), (m, two_i, H), (m, two_i)) for m in (2, 2, 1)]
     want += [(m * H, (m, H, I), (m, H, I), (m, H)) for m in (4, 1)]
     assert seen == want
+
+
+def test_the_4_bit_layer_holds_no_buffer_for_the_norm(stub):
+    """Who calls forward alone pays nothing for forward_residual."""
+    bank = moe.DeviceBank.from_tensors({"gu": torch.zeros(1), "dn": torch.zeros(1)}, E, H, I)
+    layer = moe.MoeLayer(H, I, E, K, 1, bank, bank, np.zeros((H, E), np.float32), T_max=8, device="cpu")
+    held = {v.untyped_storage().data_ptr(): v.untyped_storage().nbytes() for v in vars(layer).values()
+            if isinstance(v, torch.Tensor)}
+    assert sum(held.values()) == 4 * H * E + 2 * 8 * (K + 1) * (H + I)   # the router, y_slots and h

@@ -139,3 +139,26 @@ def test_bank_of_more_rows_than_the_quantiser_takes_at_once():
     for e in range(n):
         moe.moe_q8_quantize(moe.NormDims(rows, H, moe.ELEM_BF16, 0.0), gu[e], one, ones)
         assert torch.equal(q[e], one) and torch.equal(s[e], ones)
+
+
+# ------------------------------------------------------------------------- the 4-bit layer and the norm
+
+@pytest.mark.parametrize("T,tile", [(1, 32), (5, 32), (40, 16), (300, 128), (700, 256)])
+def test_residual_layer_in_4_bits_over_its_kernels(T, tile):
+    """The norm's rows lie in the layer's own buffers: the bits of the separate calls, twice in a row."""
+    from synth import build_config
+    c = build_config("tiny16")
+    sh = c["shape"]
+    layer = moe.MoeLayer(sh.H, sh.I, sh.E, sh.k, sh.n_shared, moe.DeviceBank(c["routed"]), moe.DeviceBank(c["shared"]),
+                         c["wr"], None, T_max=T, tile_m_max=tile)
+    g = torch.Generator("cuda").manual_seed(T)
+    x, res = (torch.randn((T, sh.H), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.linspace(0.5, 1.5, sh.H, device="cuda")
+    s, xn, want, y = (torch.empty_like(x) for _ in range(4))
+    moe.moe_add_rmsnorm(moe.NormDims(T, sh.H, moe.ELEM_BF16, 1e-6), x, res, w, s, xn)
+    layer.forward(xn, want)
+    for _ in range(2):
+        r = res.clone()
+        layer.forward_residual(x, r, w, y)
+        torch.cuda.synchronize()
+        assert torch.equal(r, s) and torch.equal(y, want) and int(layer.rt.status.item()) == 0

@@ -666,7 +666,8 @@ class MoeLayer:
         rows = T_max * k + (T_max if n_shared else 0)
         self.h = torch.empty((rows, I), dtype=torch.int16, device=device)
         self.y_slots = torch.empty((rows, H), dtype=torch.int16, device=device)
-        self.xn = torch.empty((T_max, H), dtype=torch.int16, device=device)  # forward_residual's normed rows
+        # forward_residual's normed rows: the router and gate/up have read them before down writes y_slots
+        self.xn = self.y_slots[:T_max]
 
     def dims(self, T):
         if T > self.T_max:
@@ -745,6 +746,7 @@ class Q8MoeLayer(MoeLayer):
         super().__init__(H, I, *args, device=device, **kw)
         self._banks()
         rows = self.h.shape[0]
+        self.xn = torch.empty((self.T_max, H), dtype=torch.int16, device=device)   # kept next to their 8-bit form
         self.xq = torch.empty((self.T_max, self.H), dtype=torch.int8, device=device)
         self.xs = torch.empty((self.T_max,), dtype=torch.float32, device=device)
         self.hq = torch.empty((rows, self.I), dtype=torch.int8, device=device)
