@@ -249,3 +249,19 @@ def test_the_4_bit_layer_holds_no_buffer_for_the_norm(stub):
     held = {v.untyped_storage().data_ptr(): v.untyped_storage().nbytes() for v in vars(layer).values()
             if isinstance(v, torch.Tensor)}
     assert sum(held.values()) == 4 * H * E + 2 * 8 * (K + 1) * (H + I)   # the router, y_slots and h
+
+
+def test_residual_layer_checks_its_output_first(stub):
+    w4 = moe.DeviceBank.from_tensors({"gu": torch.zeros(1), "dn": torch.zeros(1)}, E, H, I)
+    for layer in (q8_layer(q8_bank(E), q8_bank(1)),
+                  moe.MoeLayer(H, I, E, K, 1, w4, w4, np.zeros((H, E), np.float32), T_max=8, device="cpu")):
+        stub.calls.clear()
+        x, res, w = torch.zeros((T, H), dtype=BF16), torch.zeros((T, H), dtype=BF16), torch.ones(H)
+        for y in (torch.zeros((T - 1, H), dtype=BF16), torch.zeros((T, H)), torch.zeros((T, 2 * H), dtype=BF16)[:, ::2]):
+            with pytest.raises(ValueError, match="^y: "):
+                layer.forward_residual(x, res, w, y, stream=0)
+        with pytest.raises(ValueError, match="exceeds"):
+            layer.forward_residual(torch.zeros((9, H), dtype=BF16), res, w, x, stream=0)
+        assert not stub.calls
+        layer.forward_residual(x, res, w, torch.zeros((T, H), dtype=torch.int16), stream=0)
+        assert stub.calls[0] == "moe_add_rmsnorm"

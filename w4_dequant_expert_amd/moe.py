@@ -723,11 +723,17 @@ class MoeLayer:
         self.ffn_combine(d, x, y, routed, shared, stream)
         return y
 
+    def _residual_dims(self, x, y):
+        """Sizes of a forward_residual call; y is checked before res is added to."""
+        d = self.dims(x.shape[0])
+        _arg(y, 2 * d.T * self.H, "y", _device(), _BF16)
+        return d
+
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
         """The layer with what stands in front of it: res += x in place, then
         the layer on the RMS norm of the sum (bfloat16 rows of at most NORM_MAX_H
         elements, one norm call)."""
-        d = self.dims(x.shape[0])
+        d = self._residual_dims(x, y)
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         stream=stream)
         return self.forward(self.xn[:d.T], y, stream=stream)
@@ -794,7 +800,7 @@ class Q8MoeLayer(MoeLayer):
         self.combine(d, y, stream)
 
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
-        d = self.dims(x.shape[0])
+        d = self._residual_dims(x, y)
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         self.xq, self.xs, stream)
         self.route(self.xn[:d.T], stream=stream)
