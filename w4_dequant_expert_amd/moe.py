@@ -36,7 +36,9 @@ ELEM_F32, ELEM_BF16, ELEM_F16 = 0, 1, 2   # MOE_ELEM_*
 NORM_MAX_T, NORM_MAX_H = 1 << 24, 16384   # moe_norm_dims
 ELEM: dict = {}   # torch dtype -> MOE_ELEM_*, filled when the library is loaded
 # the torch types that the arrays of each kind may have, and (bytes, types) of each row type; set with ELEM
-_F32 = _I8 = _BF16 = _ROW_TYPES = ()
+_F32 = _I8 = _BF16 = ()
+_ROW_TYPES: dict = {}
+_UNKNOWN = (0, None)   # a row type that the C side refuses
 
 
 class GdnDims(ctypes.Structure):
@@ -90,7 +92,7 @@ _cuda_ready = False
 
 
 def lib():
-    global _lib, _torch, _get_device, _raw_stream, _F32, _I8, _BF16, _ROW_TYPES
+    global _lib, _torch, _get_device, _raw_stream, _F32, _I8, _BF16
     if _lib is None:
         # torch ships its own HIP runtime.  Import it first so that loading the
         # library resolves libamdhip64.so.7 to that same runtime; loading the
@@ -172,7 +174,7 @@ def lib():
         ELEM.update({torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.float16: ELEM_F16})
         bits = (torch.int16, torch.uint16)
         _F32, _I8, _BF16 = (torch.float32,), (torch.int8,), (torch.bfloat16, *bits)
-        _ROW_TYPES = ((4, _F32), (2, _BF16), (2, (torch.float16, *bits)))
+        _ROW_TYPES.update({ELEM_F32: (4, _F32), ELEM_BF16: (2, _BF16), ELEM_F16: (2, (torch.float16, *bits))})
         _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _lib, _torch = L, torch
     return _lib
@@ -340,11 +342,6 @@ def gdn_scan_chunked(d: GdnDims, q, k, v, g, beta, state_in, state_out, o, ws, w
 
 # ------------------------------------------- around the expert layer (include/moe_block.h)
 
-def _row_type(elem: int):
-    """Bytes and torch types of a row type; an unknown one is refused by the C side."""
-    return _ROW_TYPES[elem] if 0 <= elem < 3 else (0, None)
-
-
 def _arg(t, nbytes: int, what: str, device: int, types=None):
     """Address of a dense array of at least nbytes on `device` (None -> NULL; raw addresses pass).
 
@@ -366,7 +363,7 @@ def moe_add_rmsnorm(d: NormDims, x, res, weight, sum, y, yq=None, ys=None, strea
     """Residual addition and RMS norm (any of res, sum, y, yq with ys may be None)."""
     dev = _device()
     n = d.T * d.H
-    size, typ = _row_type(d.type)
+    size, typ = _ROW_TYPES.get(d.type, _UNKNOWN)
     row = n * size
     _check(_lib.moe_add_rmsnorm(d, _arg(x, row, "x", dev, typ), _arg(res, row, "res", dev, typ),
                                 _arg(weight, 4 * d.H, "weight", dev, _F32), _arg(sum, row, "sum", dev, typ),
@@ -382,7 +379,7 @@ def moe_add_rmsnorm_backward(d: NormDims, sum, weight, dy, dsum, dx, dweight, ws
                              stream=None):
     """Gradients of moe_add_rmsnorm (dsum and dweight may be None)."""
     dev = _device()
-    size, typ = _row_type(d.type)
+    size, typ = _ROW_TYPES.get(d.type, _UNKNOWN)
     row = d.T * d.H * size
     _check(_lib.moe_add_rmsnorm_backward(
         d, _arg(sum, row, "sum", dev, typ), _arg(weight, 4 * d.H, "weight", dev, _F32),
@@ -395,7 +392,7 @@ def moe_q8_quantize(d: NormDims, x, xq, xs, stream=None):
     """Rows to int8 with a scale per row."""
     dev = _device()
     n = d.T * d.H
-    size, typ = _row_type(d.type)
+    size, typ = _ROW_TYPES.get(d.type, _UNKNOWN)
     _check(_lib.moe_q8_quantize(d, _arg(x, n * size, "x", dev, typ), _arg(xq, n, "xq", dev, _I8),
                                 _arg(xs, 4 * d.T, "xs", dev, _F32), _stream(stream, dev)),
            "moe_q8_quantize")
@@ -404,7 +401,7 @@ def moe_q8_quantize(d: NormDims, x, xq, xs, stream=None):
 def moe_q8_matmul(d: Q8Dims, xq, xs, wq, ws, out, stream=None):
     """Dense product of 8-bit integers with token and channel scales."""
     dev = _device()
-    size, typ = _row_type(d.type)
+    size, typ = _ROW_TYPES.get(d.type, _UNKNOWN)
     _check(_lib.moe_q8_matmul(d, _arg(xq, d.M * d.K, "xq", dev, _I8), _arg(xs, 4 * d.M, "xs", dev, _F32),
                               _arg(wq, d.N * d.K, "wq", dev, _I8), _arg(ws, 4 * d.N, "ws", dev, _F32),
                               _arg(out, d.M * d.N * size, "out", dev, typ), _stream(stream, dev)),
@@ -435,7 +432,7 @@ def moe_q8_down(d: Dims, out: RouteOut, routed: Q8Bank, shared, hq, hs, y_slots,
 def moe_dispatch_rows(d: Dims, elem: int, x, out: RouteOut, rows, stream=None):
     """Token rows into moe_route's order (elem: one of ELEM_*)."""
     dev = _device()
-    size, typ = _row_type(elem)
+    size, typ = _ROW_TYPES.get(elem, _UNKNOWN)
     e = size * d.H
     _check(_lib.moe_dispatch_rows(d, elem, _arg(x, d.T * e, "x", dev, typ), out,
                                   _arg(rows, _rows_of(d) * e, "rows", dev, typ), _stream(stream, dev)),
@@ -444,7 +441,7 @@ def moe_dispatch_rows(d: Dims, elem: int, x, out: RouteOut, rows, stream=None):
 
 def moe_dispatch_rows_backward(d: Dims, elem: int, drows, out: RouteOut, dx, stream=None):
     dev = _device()
-    size, typ = _row_type(elem)
+    size, typ = _ROW_TYPES.get(elem, _UNKNOWN)
     e = size * d.H
     _check(_lib.moe_dispatch_rows_backward(d, elem, _arg(drows, _rows_of(d) * e, "drows", dev, typ),
                                            out, _arg(dx, d.T * e, "dx", dev, typ),
@@ -454,7 +451,7 @@ def moe_dispatch_rows_backward(d: Dims, elem: int, drows, out: RouteOut, dx, str
 def moe_combine_rows(d: Dims, elem: int, rows, out: RouteOut, y, stream=None):
     """moe_combine for any row type."""
     dev = _device()
-    size, typ = _row_type(elem)
+    size, typ = _ROW_TYPES.get(elem, _UNKNOWN)
     e = size * d.H
     _check(_lib.moe_combine_rows(d, elem, _arg(rows, _rows_of(d) * e, "rows", dev, typ),
                                  out, _arg(y, d.T * e, "y", dev, typ), _stream(stream, dev)),
@@ -465,7 +462,7 @@ def moe_combine_rows_backward(d: Dims, elem: int, dy, rows, out: RouteOut, drows
                               stream=None):
     """Gradients of the combine (dtopk_w None: rows is not read and may be None)."""
     dev = _device()
-    size, typ = _row_type(elem)
+    size, typ = _ROW_TYPES.get(elem, _UNKNOWN)
     e = size * d.H
     _check(_lib.moe_combine_rows_backward(d, elem, _arg(dy, d.T * e, "dy", dev, typ),
                                           _arg(rows, _rows_of(d) * e, "rows", dev, typ), out,
