@@ -61,8 +61,9 @@ typedef struct moe_norm_dims {
  *   y       [T][H] rounded once to the row type (16-byte aligned), or NULL;
  *           may be x or res itself, but not sum
  *   yq, ys  [T][H] int8 (16-byte aligned) and [T] float32 (4-byte aligned):
- *           ys = max|y| / 127 and yq = y / ys rounded to the nearest integer
- *           (ties to even), from y before its rounding; both or neither NULL
+ *           ys = max|y| / 127 and yq = y (127 / max|y|), in float32, rounded to
+ *           the nearest integer (ties to even), from y before its rounding; both
+ *           or neither NULL
  * At least one of y and yq.  The sum, the statistics and y are float32; the
  * norm reads s before its rounding.  Row sums of squares past float32's range
  * (elements above about 1e19) give rows of zeros, as float32 arithmetic does.

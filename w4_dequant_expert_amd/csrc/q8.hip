@@ -11,7 +11,7 @@
 //   q8_stream_kernel: few rows.  Bound by reading the weights once; every wave
 //     streams its share of K straight from memory into the matrix operands,
 //     with no LDS and no barrier until the waves' sums are added.  One row of
-//     2048 times 8192 columns: 4.9 us, 3.4 TB/s.
+//     2048 times 8192 columns: 5.1 us, 3.3 TB/s.
 //   q8_tile_kernel: more rows.  Tiles of both operands go through LDS in steps
 //     of 128 inputs.  Bound by the weights' bytes up to some hundred rows a
 //     matrix (512 tokens over 256 experts: 5.1 to 5.3 TB/s), then by what the
@@ -275,9 +275,9 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8, a
 // row of the grid being a multiple of 8) in contiguous runs, so that the tiles an XCD works on together share rows and
 // columns in its own L2: a dense run goes through groups of four row blocks
-// column by column (8192 cubed: groups of one 537 us, two 511, four 493, eight
-// 494), a grouped one block by block (16384 tokens: 426 us, in groups of four
-// 434), since neighbouring blocks mostly have other weights.
+// column by column (8192 cubed: groups of one 513 us, two 467, four 456, eight
+// 461), a grouped one block by block (gate/up of 16384 tokens: 411 us, in groups
+// of four 424), since neighbouring blocks mostly have other weights.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 constexpr int kNonTemporal = 2;  // cache policy of a copy whose data nobody else reads
@@ -642,10 +642,12 @@ void launch_tile(const Q8Args& a, int blocks, hipStream_t s) {
 // else the largest tile that still gives every CU (256) a workgroup, and below
 // that the smallest tile, with four buffers in flight where even those are few.
 // Measured at K = 2048, us:        64x8192  333x2048  333x8192  1000x8192  2048x2048
-//   64 x 64, four buffers              8.5       8.4      18.1       40.0       20.7
-//   64 x 64, two buffers              11.1      10.3      14.2       32.8       17.2
-//   128 x 128                         11.6      11.4      14.9       23.0       15.9
-// and 16384x8192: 256 x 256 282 (1.95 PFLOP/s; 2.44 at 8192 cubed), 128 x 128 345.
+//   64 x 64, four buffers              8.8       8.6      17.7       39.1       21.3
+//   64 x 64, two buffers              11.4      11.0      13.8       32.1       18.1
+//   128 x 128                         12.9      12.3      16.1       23.7       17.2
+// and 16384x8192: 256 x 256 260 (2.1 PFLOP/s; 2.4 at 8192 cubed), 128 x 128 335.
+// The rule counts tiles, not rows: 64 rows of 65536 columns take the largest tile
+// (34 us), although the other two are faster there (31 and 32).
 hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
   const auto tiles = [&](int bm, int bn) { return static_cast<long long>(cdiv(a.rows, bm)) * cdiv(a.N, bn); };
   if (a.rows <= 16) {
@@ -672,19 +674,25 @@ hipError_t launch_dense(const Q8Args& a, hipStream_t s) {
 // expert holds every token, another expert a few times the mean, and the map
 // cuts both at tile_m_max.  A block taller than the kernel's tile takes several
 // passes and ends last; a tile much taller than the blocks holds less of the
-// weights in flight.  Measured on gate/up of 256 experts of 2048 x 1024, eight
-// each and a shared one, us by tokens/tile_m_max:
+// weights in flight.  Measured on 256 experts of 2048 x 512, eight each and a
+// shared one, us by tokens/tile_m_max:
 //               128/128  256/128  512/32  512/128  1024/128  2048/128  2048/256  4096/256  16384/256
-//   stream          99      127     154      180       273       461       508       872
-//   32 x 128        93      109     103      140       184       288       324       539       894
-//   64 x 256        82       90     103      115       140       188       210       318       537
-//   128 x 128       91       98     123      106       122       145       159       216       502
-//   256 x 256      103      107     134      114       134       153       155       186       437
-// (128 tokens in blocks of at most 32: stream 82, 32 x 128 84; 512 in blocks of
-// at most 16: stream 146, 32 x 128 123.  All rows were measured with one deal of
-// the tiles; dealt block by block, as now, the largest tile takes 144 at
-// 2048/256, 186 at 4096/128 and 411 at 16384/256.)  Weights that are read once
-// are copied past the caches (512 tokens, down: 60 us -> 57).
+//   gate/up (1024 columns, K = 2048)
+//   stream           98      129     154      179       272       458       509       868
+//   32 x 128         97      111     104      130       173       267       291       485       878
+//   64 x 256         80       90     101      103       135       173       190       287       537
+//   128 x 128        85       90     112       95       112       131       139       185       477
+//   256 x 256        90       95     118      101       120       140       138       168       411
+//   down (2048 columns, K = 512)
+//   stream           49       63      80       88       136       231       250       437
+//   32 x 128         50       56      58       68        91       140       156       253       508
+//   64 x 256         49       52      60       60        73        94       103       159       366
+//   128 x 128        50       57      74       64        70        81        84       127       372
+//   256 x 256        52       60      77       66        73        83        82       121       333
+// (gate/up of 128 tokens in blocks of at most 32: stream 82, 32 x 128 74; of 512 in
+// blocks of at most 16: 146, 122; of 4096 in blocks of at most 128: 128 x 128 176,
+// 256 x 256 194.)  Weights that are read once are copied past the caches (512/32:
+// gate/up 105 us -> 100, down 61 -> 57).
 template <bool GATHER, bool SWIGLU>
 hipError_t launch_grouped(const moe_dims& d, const Q8Args& a, hipStream_t s) {
   const int mean = cdiv(d.T * d.k, d.E);

@@ -15,9 +15,10 @@
 // 16-byte accesses.  Slot positions and weights are workgroup-uniform.  Sorted
 // rows of large batches are streamed past the caches (kStreamStore, kStreamLoad
 // in block.h).  Measured at 8192 tokens of 2048 bfloat16, 8 + 1 rows a token
-// (335 MB moved, 637 MB for the combine's gradient), us plain -> streamed:
-// dispatch 68 -> 53, combine 65 -> 57, its gradient 123 -> 108, the dispatch's
-// 65 -> 57: 5.9 to 6.3 TB/s, the rate of a plain streaming read (5.85).
+// (335 MB moved, 604 MB for the combine's gradient, which does not read the
+// shared rows), us plain -> streamed: dispatch 68 -> 53, combine 65 -> 57, its
+// gradient 123 -> 108, the dispatch's 65 -> 57: 6.3, 5.9, 5.6 and 5.9 TB/s, about
+// the rate of a plain streaming read (5.85).
 #include "block.h"
 
 namespace moe {
