@@ -137,7 +137,7 @@ def test_layer_refuses_banks_that_are_not_its_own_size(stub):
         with pytest.raises(ValueError, match="^routed: "):
             q8_layer(routed, q8_bank(1))
         with pytest.raises(ValueError, match="^routed: "):
-            layer._gate_up_quantised(d, routed=routed, stream=0)
+            layer.gate_up(d, x, routed=routed, stream=0)
         with pytest.raises(ValueError, match="^routed: "):
             layer.down(d, routed=routed, stream=0)
     for shared in (q8_bank(0), q8_bank(1, h=H + 64), q8_bank(1, i=2 * I)):
@@ -146,11 +146,17 @@ def test_layer_refuses_banks_that_are_not_its_own_size(stub):
         with pytest.raises(ValueError, match="^shared: "):
             layer.down(d, shared=shared, stream=0)
     assert not {"moe_q8_gate_up", "moe_q8_down"} & set(stub.calls)
+    # without a shared expert none is read, whatever is at hand
     q8_layer(q8_bank(E), None, n_shared=0)
+    q8_layer(q8_bank(E), q8_bank(1, h=H + 64), n_shared=0).down(d, shared=q8_bank(0), stream=0)
+    stub.calls.clear()
     # replaced on the layer itself
     layer.routed = q8_bank(1)
     with pytest.raises(ValueError, match="^routed: "):
         layer.forward(x, y, stream=0)
+    with pytest.raises(ValueError, match="^routed: "):
+        layer.forward_residual(x, x.clone(), torch.ones(H), y, stream=0)
+    assert "moe_add_rmsnorm" not in stub.calls
 
 
 def test_bank_refuses_an_odd_count_of_gate_and_up_rows(stub):

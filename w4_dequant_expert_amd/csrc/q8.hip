@@ -273,11 +273,12 @@ __global__ __launch_bounds__(64 * W) void q8_stream_kernel(Q8Args a) {
 // they only reach outputs that are not stored.
 //
 // Tiles are dealt to the chip's eight XCDs (workgroup i runs on XCD i mod 8, a
-// row of the grid being a multiple of 8) in contiguous runs, so that the tiles an XCD works on together share rows and
-// columns in its own L2: a dense run goes through groups of four row blocks
-// column by column (8192 cubed: groups of one 513 us, two 467, four 456, eight
-// 461), a grouped one block by block (gate/up of 16384 tokens: 411 us, in groups
-// of four 424), since neighbouring blocks mostly have other weights.
+// row of the grid being a multiple of 8) in contiguous runs, so that the tiles
+// an XCD works on together share rows and columns in its own L2: a dense run
+// goes through groups of four row blocks column by column (8192 cubed: groups of
+// one 513 us, two 467, four 456, eight 461), a grouped one block by block
+// (gate/up of 16384 tokens: 411 us, in groups of four 424), since neighbouring
+// blocks mostly have other weights.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 constexpr int kNonTemporal = 2;  // cache policy of a copy whose data nobody else reads

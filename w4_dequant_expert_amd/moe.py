@@ -756,36 +756,38 @@ class Q8MoeLayer(MoeLayer):
         self.hs = torch.empty((rows,), dtype=torch.float32, device=device)
 
     def gate_up(self, d, x, routed=None, shared=None, stream=None):
-        moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
-        self._gate_up_quantised(d, routed, shared, stream)
+        self._gate_up(d, self._banks(routed, shared), x, stream)
+
+    def down(self, d, routed=None, shared=None, stream=None):
+        self._down(d, self._banks(routed, shared), stream)
+
+    def ffn(self, d, x, routed=None, shared=None, stream=None):
+        banks = self._banks(routed, shared)
+        self._gate_up(d, banks, x, stream)
+        self._down(d, banks, stream)
 
     def _banks(self, routed=None, shared=None):
         """The C structs of the banks of a call (None: the layer's own); the kernels read them by the
         layer's sizes."""
-        out = []
-        for what, bank, n in (("routed", routed or self.routed, self.E), ("shared", shared or self.shared, 1)):
+        routed, shared = routed or self.routed, (shared or self.shared) if self.n_shared else None
+        for what, bank, n in (("routed", routed, self.E), ("shared", shared, 1)):
             if bank is not None and not (isinstance(bank, DeviceBankQ8) and bank.n >= n and bank.H == self.H and
-                                         bank.I == self.I and bank.t["gu"].device == self.h.device):
+                                         bank.I == self.I and bank.t["gu"].get_device() == self.h.get_device()):
                 raise ValueError(f"{what}: a DeviceBankQ8 of {n} experts, H {self.H}, I {self.I} on {self.h.device} "
                                  f"is needed, got {bank}")
-            out.append(None if bank is None else bank.c)
-        return out
+        return None if routed is None else routed.c, None if shared is None else shared.c
 
-    def _gate_up_quantised(self, d, routed=None, shared=None, stream=None):
-        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, *self._banks(routed, shared), self.h, stream)
+    def _gate_up(self, d, banks, x, stream):
+        moe_q8_quantize(NormDims(d.T, self.H, ELEM_BF16, 0.0), x, self.xq, self.xs, stream)
+        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, *banks, self.h, stream)
 
-    def down(self, d, routed=None, shared=None, stream=None):
-        banks = self._banks(routed, shared)
+    def _down(self, d, banks, stream):
         rows = _rows_of(d)
         moe_q8_quantize(NormDims(min(rows, NORM_MAX_T), self.I, ELEM_BF16, 0.0), self.h, self.hq, self.hs, stream)
         for lo in range(NORM_MAX_T, rows, NORM_MAX_T):   # up to 33 * 2^20 rows
             moe_q8_quantize(NormDims(min(rows - lo, NORM_MAX_T), self.I, ELEM_BF16, 0.0), self.h[lo:], self.hq[lo:],
                             self.hs[lo:], stream)
         moe_q8_down(d, self.rt.c, *banks, self.hq, self.hs, self.y_slots, stream)
-
-    def ffn(self, d, x, routed=None, shared=None, stream=None):
-        self.gate_up(d, x, routed, shared, stream)
-        self.down(d, routed, shared, stream)
 
     def shared_ffn(self, d, x, shared=None, stream=None):
         raise NotImplementedError("the 8-bit layer has no split of the shared expert")
@@ -797,11 +799,11 @@ class Q8MoeLayer(MoeLayer):
         self.combine(d, y, stream)
 
     def forward_residual(self, x, res, norm_weight, y, eps=1e-6, stream=None):
-        d = self._residual_dims(x, y)
+        d, banks = self._residual_dims(x, y), self._banks()
         moe_add_rmsnorm(NormDims(d.T, self.H, ELEM_BF16, eps), x, res, norm_weight, res, self.xn,
                         self.xq, self.xs, stream)
         self.route(self.xn[:d.T], stream=stream)
-        self._gate_up_quantised(d, stream=stream)
-        self.down(d, stream=stream)
+        moe_q8_gate_up(d, self.xq, self.xs, self.rt.c, *banks, self.h, stream)
+        self._down(d, banks, stream)
         self.combine(d, y, stream)
         return y
